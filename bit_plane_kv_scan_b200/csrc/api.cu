@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "fathom_internal.cuh"
+#include "kv_attention.cuh"
 
 namespace fathom {
 cudaError_t launch_pack(const uint8_t *codes, int64_t n, int d, int h_kv, uint32_t *planes,
@@ -31,6 +32,9 @@ cudaError_t launch_merge_parts(const int32_t *in_idx, const float *in_score, int
                                const int64_t *offsets, int h_q, int k_in, int k, int32_t *out_idx,
                                float *out_score, cudaStream_t stream);
 int tc_plan_bytes(int d);
+cudaError_t launch_kv_append(const fathom_kv_append_args *a, const KvBatch &b, cudaStream_t stream);
+void plan_kv_attention(KvAttnParams &a);
+cudaError_t launch_kv_attention(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
 }  // namespace fathom
 
 using namespace fathom;
@@ -164,6 +168,139 @@ fathom_status check_scan_common(int64_t n, int d, int h_q, int h_kv, int k, int 
   REQUIRE(planes_location == FATHOM_PLANES_DEVICE || planes_location == FATHOM_PLANES_HOST_MAPPED,
           "planes_location=%d unknown", planes_location);
   return FATHOM_OK;
+}
+
+// ---------------------------------------------------------- paged KV cache --
+// The current device: the calls on a paged cache check that every pointer
+// belongs to it, since their launches go there.
+fathom_status check_on_device(const void *p, const char *name, size_t align) {
+  if (p == nullptr) return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s is not a device pointer", name);
+  }
+  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
+    return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s is not a device pointer", name);
+  int dev = 0;
+  if (a.type == cudaMemoryTypeDevice && cudaGetDevice(&dev) == cudaSuccess && a.device != dev)
+    return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s is on device %d, the current device is %d", name,
+                a.device, dev);
+  if (!aligned(p, align))
+    return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s must be %zu-byte aligned", name, align);
+  return FATHOM_OK;
+}
+
+#define REQUIRE_ON_DEVICE(ptr, name, align)                         \
+  do {                                                              \
+    const fathom_status st_ = check_on_device((ptr), (name), (align)); \
+    if (st_ != FATHOM_OK) return st_;                               \
+  } while (0)
+
+size_t elt_size(int dtype) { return dtype == FATHOM_F32 ? 4 : dtype == FATHOM_BF16 ? 2 : 1; }
+
+// Shapes and bounds of a cache and a batch (no pointers).
+fathom_status check_kv_shape(const fathom_kv_cache &c, const fathom_kv_batch &b) {
+  REQUIRE(c.dtype == FATHOM_BF16 || c.dtype == FATHOM_E4M3, "cache dtype=%d unknown", c.dtype);
+  if (c.d < 32 || c.d > FATHOM_MAX_D || c.d % 32 != 0)
+    return fail(FATHOM_ERR_UNSUPPORTED, "d=%d: need a multiple of 32 in [32, %d]", c.d, FATHOM_MAX_D);
+  REQUIRE(c.h_kv >= 1 && c.h_kv <= 65535, "h_kv=%d out of range [1, 65535]", c.h_kv);
+  REQUIRE(c.num_pages >= 1, "num_pages=%d: need >= 1", c.num_pages);
+  REQUIRE(c.page_tokens >= FATHOM_KV_BLOCK && c.page_tokens % FATHOM_KV_BLOCK == 0 &&
+              c.page_tokens <= FATHOM_KV_MAX_LEN,
+          "page_tokens=%d: need a multiple of %d in [%d, %d]", c.page_tokens, FATHOM_KV_BLOCK,
+          FATHOM_KV_BLOCK, FATHOM_KV_MAX_LEN);
+  REQUIRE(b.num_seqs >= 0 && b.num_seqs <= (1 << 24), "num_seqs=%d out of range [0, 2^24]",
+          b.num_seqs);
+  REQUIRE(b.table_width >= 0, "table_width=%d is negative", b.table_width);
+  REQUIRE(b.num_rows >= 0 && b.num_rows <= FATHOM_KV_MAX_LEN, "num_rows=%d out of range [0, %d]",
+          b.num_rows, FATHOM_KV_MAX_LEN);
+  REQUIRE(b.max_rows >= 0 && b.max_rows <= b.num_rows, "max_rows=%d out of range [0, num_rows=%d]",
+          b.max_rows, b.num_rows);
+  REQUIRE(b.max_len >= 0 && b.max_len <= FATHOM_KV_MAX_LEN, "max_len=%lld out of range [0, %d]",
+          (long long)b.max_len, FATHOM_KV_MAX_LEN);
+  REQUIRE(b.q_start != nullptr || (b.num_rows == b.num_seqs && (b.max_rows == 1 || b.num_rows == 0)),
+          "without q_start every sequence has one row: num_rows=%d num_seqs=%d max_rows=%d",
+          b.num_rows, b.num_seqs, b.max_rows);
+  return FATHOM_OK;
+}
+
+fathom_status check_kv_pointers(const fathom_kv_cache &c, const fathom_kv_batch &b) {
+  REQUIRE_ON_DEVICE(c.k, "cache.k", 16);
+  REQUIRE_ON_DEVICE(c.v, "cache.v", 16);
+  if (c.dtype == FATHOM_E4M3) {
+    REQUIRE_ON_DEVICE(c.k_scale, "cache.k_scale", 1);
+    REQUIRE_ON_DEVICE(c.v_scale, "cache.v_scale", 1);
+  }
+  REQUIRE_ON_DEVICE(b.seq_len, "batch.seq_len", 4);
+  if (b.table_width > 0) REQUIRE_ON_DEVICE(b.page_table, "batch.page_table", 4);
+  if (b.q_start) REQUIRE_ON_DEVICE(b.q_start, "batch.q_start", 4);
+  return FATHOM_OK;
+}
+
+KvBatch kv_batch_of(const fathom_kv_cache &c, const fathom_kv_batch &b) {
+  KvBatch x;
+  x.page_table = b.page_table;
+  x.seq_len = b.seq_len;
+  x.q_start = b.q_start;
+  x.num_seqs = b.num_seqs;
+  x.table_width = b.table_width;
+  x.num_rows = b.num_rows;
+  x.max_rows = b.max_rows;
+  x.max_len = (int)b.max_len;
+  x.num_pages = c.num_pages;
+  x.page_tokens = c.page_tokens;
+  x.h_kv = c.h_kv;
+  return x;
+}
+
+fathom_status check_rows(const char *name, int dtype, int heads, int d, int64_t stride) {
+  REQUIRE(dtype == FATHOM_F32 || dtype == FATHOM_BF16, "%s dtype=%d unknown", name, dtype);
+  REQUIRE(stride == 0 || stride >= (int64_t)heads * d,
+          "%s stride=%lld: rows of %d heads overlap (0 stands for contiguous)", name,
+          (long long)stride, heads);
+  return FATHOM_OK;
+}
+
+// Everything about an attention call but its pointers, and its plan.
+fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams &p) {
+  REQUIRE(a != nullptr, "args is NULL");
+  fathom_status st = check_kv_shape(a->cache, a->batch);
+  if (st != FATHOM_OK) return st;
+  REQUIRE(a->h_q >= 1 && a->h_q % a->cache.h_kv == 0, "h_q=%d is not a multiple of h_kv=%d", a->h_q,
+          a->cache.h_kv);
+  st = check_rows("q", a->q_dtype, a->h_q, a->cache.d, a->q_stride);
+  if (st != FATHOM_OK) return st;
+  REQUIRE(std::isfinite(a->softmax_scale), "softmax_scale is not finite");
+  REQUIRE(a->window >= 0, "window=%lld is negative", (long long)a->window);
+  REQUIRE(a->sinks >= 0, "sinks=%lld is negative", (long long)a->sinks);
+  memset(&p, 0, sizeof(p));
+  p.b = kv_batch_of(a->cache, a->batch);
+  p.h_q = a->h_q;
+  p.G = a->h_q / a->cache.h_kv;
+  p.q_bf16 = a->q_dtype == FATHOM_BF16;
+  p.q_stride = a->q_stride ? a->q_stride : (int64_t)a->h_q * a->cache.d;
+  p.qscale = a->softmax_scale * 1.4426950408889634f;
+  const int64_t all = FATHOM_KV_MAX_LEN;
+  p.window = (int)(a->window == 0 || a->window > all ? all : a->window);
+  p.sinks = (int)(a->sinks > all ? all : a->sinks);
+  if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return FATHOM_OK;
+  if ((int64_t)a->batch.max_rows * p.G > FATHOM_KV_MAX_LEN)
+    return fail(FATHOM_ERR_UNSUPPORTED, "max_rows=%d times %d heads a KV head is too many",
+                a->batch.max_rows, p.G);
+  plan_kv_attention(p);
+  if ((double)p.b.num_seqs * p.b.h_kv * p.col_tiles * p.splits >= 2147483647.0)
+    return fail(FATHOM_ERR_UNSUPPORTED,
+                "num_seqs=%d max_rows=%d h_q=%d: too many blocks for one launch", p.b.num_seqs,
+                p.b.max_rows, p.h_q);
+  return FATHOM_OK;
+}
+
+// The workspace: status, then the splits' maxima and sums, then their outputs.
+size_t kv_workspace(const KvAttnParams &p, int d, size_t *off_o) {
+  const size_t parts = p.splits > 1 ? (size_t)p.splits * p.b.num_rows * p.h_q : 0;
+  *off_o = sizeof(WsStatus) + up256(parts * 8);
+  return *off_o + up256(parts * d * 4);
 }
 
 }  // namespace
@@ -508,6 +645,88 @@ fathom_status fathom_scan_read_report(const void *ws, fathom_scan_report *report
   report->union_planes = hs.union_planes;
   if (hs.device_faults) return fail(FATHOM_ERR_DEVICE_CHECK, "device checks recorded %u faults",
                                     hs.device_faults);
+  return ok();
+}
+
+fathom_status fathom_kv_append(const fathom_kv_append_args *a, void *stream) {
+  const CallRange range("fathom_kv_append");
+  REQUIRE(a != nullptr, "args is NULL");
+  fathom_status st = check_kv_shape(a->cache, a->batch);
+  if (st != FATHOM_OK) return st;
+  const int d = a->cache.d, h_kv = a->cache.h_kv;
+  st = check_rows("k and v", a->kv_dtype, h_kv, d, a->k_stride);
+  if (st == FATHOM_OK) st = check_rows("k and v", a->kv_dtype, h_kv, d, a->v_stride);
+  if (st != FATHOM_OK) return st;
+  if (a->q) {
+    REQUIRE(a->h_q >= 1, "h_q=%d: need >= 1", a->h_q);
+    st = check_rows("q", a->q_dtype, a->h_q, d, a->q_stride);
+    if (st != FATHOM_OK) return st;
+  }
+  REQUIRE(a->rotary_pairs >= 0 && 2 * (int64_t)a->rotary_pairs <= d,
+          "rotary_pairs=%d out of range [0, d/2=%d]", a->rotary_pairs, d / 2);
+  REQUIRE(a->rotary_pairs == 0 || a->inv_freq != nullptr, "inv_freq is NULL");
+  if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return ok();
+  st = check_kv_pointers(a->cache, a->batch);
+  if (st != FATHOM_OK) return st;
+  REQUIRE_ON_DEVICE(a->k, "k", elt_size(a->kv_dtype));
+  REQUIRE_ON_DEVICE(a->v, "v", elt_size(a->kv_dtype));
+  if (a->rotary_pairs) REQUIRE_ON_DEVICE(a->inv_freq, "inv_freq", 4);
+  if (a->q) {
+    const size_t el = elt_size(a->q_dtype);
+    REQUIRE_ON_DEVICE(a->q, "q", el);
+    REQUIRE_ON_DEVICE(a->q_out, "q_out", el);
+    const int64_t rows = a->batch.num_rows, row = (int64_t)a->h_q * d;
+    const int64_t stride = a->q_stride ? a->q_stride : row;
+    const uintptr_t q0 = (uintptr_t)a->q, o0 = (uintptr_t)a->q_out;
+    const uintptr_t q1 = q0 + (uintptr_t)((rows - 1) * stride + row) * el;
+    const uintptr_t o1 = o0 + (uintptr_t)(rows * row) * el;
+    REQUIRE(q1 <= o0 || o1 <= q0 || (q0 == o0 && stride == row),
+            "q_out overlaps q without being q");
+  }
+  cudaError_t e = launch_kv_append(a, kv_batch_of(a->cache, a->batch), (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return ok();
+}
+
+size_t fathom_kv_attention_workspace_size(const fathom_kv_attention_args *a) {
+  KvAttnParams p;
+  if (check_kv_attention(a, p) != FATHOM_OK) return 0;
+  size_t off_o;
+  return kv_workspace(p, a->cache.d, &off_o);
+}
+
+fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, size_t ws_bytes,
+                                  void *stream) {
+  const CallRange range("fathom_kv_attention");
+  KvAttnParams p;
+  fathom_status st = check_kv_attention(a, p);
+  if (st != FATHOM_OK) return st;
+  if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return ok();
+  st = check_kv_pointers(a->cache, a->batch);
+  if (st != FATHOM_OK) return st;
+  const size_t el = elt_size(a->q_dtype);
+  REQUIRE_ON_DEVICE(a->q, "q", el);
+  REQUIRE_ON_DEVICE(a->out, "out", el);
+  if (a->lse) REQUIRE_ON_DEVICE(a->lse, "lse", 4);
+  REQUIRE_ON_DEVICE(ws, "workspace", 256);
+  size_t off_o;
+  const size_t need = kv_workspace(p, a->cache.d, &off_o);
+  if (ws_bytes < need)
+    return fail(FATHOM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  p.ck = a->cache.k;
+  p.cv = a->cache.v;
+  p.k_scale = a->cache.k_scale;
+  p.v_scale = a->cache.v_scale;
+  p.q = a->q;
+  p.out = a->out;
+  p.lse = a->lse;
+  unsigned char *base = static_cast<unsigned char *>(ws);
+  p.status = reinterpret_cast<WsStatus *>(base);
+  p.part_ml = reinterpret_cast<float2 *>(base + sizeof(WsStatus));
+  p.part_o = reinterpret_cast<float *>(base + off_o);
+  cudaError_t e = launch_kv_attention(p, a->cache.d, a->cache.dtype == FATHOM_E4M3,
+                                      (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
   return ok();
 }
 

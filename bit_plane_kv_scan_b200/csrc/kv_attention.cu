@@ -1,0 +1,519 @@
+// fathom_kv_attention, few rows: the attention of one or a few new tokens of
+// each sequence over its paged cache.
+//
+// Row at position p and query head h: s_j = scale <q, k_j> over the visible j,
+// out = sum_j softmax(s)_j v_j, lse = log sum_j exp(s_j).  One pass over K and V
+// with a running maximum and sum, 16 keys at a time.
+//
+// Bound by the bytes of K and V: with G heads a KV head, 4 G operations per
+// element.  At 23 bytes a clock and SM that is more than the fp32 units have
+// left beside unpacking, so both products run as m16n8k16 MMAs with keys (then
+// dimensions) as the 16 rows and up to 8 (token, head) pairs as the 8 columns.
+// (The tcgen05 MMAs need 64 rows or more of one operand in shared memory and an
+// accumulator in tensor memory; with 8 columns of work their set-up costs more
+// than the product.)  The order of the contracted index is free, so K and V go
+// straight from global memory into the registers that the MMAs read, 16 bytes a
+// lane, without shared memory:
+//   S^T = K q^T: lane (g, t) holds, of keys g and g + 8, the row's pieces t of
+//     every four; q's fragments are permuted in the same way.
+//   O^T = V^T P^T: lane (g, t) holds, of keys 2t, 2t + 1, 2t + 8, 2t + 9, the
+//     row's pieces g of every eight; byte permutes pair two keys' elements.
+//     P^T comes from S^T by movmatrix.
+// Each warp takes every fourth 16-key tile of its block's run of tiles and loads
+// the next one while it works on the current one.  The four warps' results meet
+// in shared memory; where a sequence's tiles are split over several blocks, a
+// second kernel joins the blocks' results (maximum, sum, output).
+//
+// E4M3: codes become fp16 exactly (the hardware's conversion).  q is scaled to
+// fp16 by a power of two per row and head; a 16-key tile is one scale block, so
+// K's scale multiplies S and V's multiplies that tile's product in fp32.
+// Softmax weights are rounded to fp16 after a factor 2^15, which keeps weights
+// down to 2^-29 of the largest to 11 bits.  bf16: weights are rounded to bf16.
+// fp32 queries: q and the weights are split into 2 (fp16) or 3 (bf16) terms and
+// the products run once for each.
+//
+// Masks: only tiles at the edge of what some column sees are masked.  There a V
+// row that a token does not see is replaced by zeros for that token, so that
+// what it holds (0 * NaN) cannot reach it.
+#include <cuda_fp8.h>
+
+#include "kv_attention.cuh"
+
+namespace fathom {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCols = 8;  // (token, head) pairs of a block: the MMA's n
+
+template <bool F8>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (F8)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Two e4m3 codes to two fp16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3_half2(uint32_t two) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(d) : "h"((uint16_t)two));
+  return d;
+}
+
+// Two floats as 16-bit terms (a in the low half); what is left goes back.
+template <bool F8>
+__device__ __forceinline__ uint32_t split16(float &a, float &b) {
+  uint32_t r;
+  if constexpr (F8) {
+    const __half2 h = __floats2half2_rn(a, b);
+    r = *reinterpret_cast<const uint32_t *>(&h);
+    a -= __low2float(h);
+    b -= __high2float(h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    r = *reinterpret_cast<const uint32_t *>(&h);
+    a -= __low2float(h);
+    b -= __high2float(h);
+  }
+  return r;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(const uint8_t *p, uint32_t *w) {
+  if constexpr (BYTES == 16) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+  } else if constexpr (BYTES == 8) {
+    asm volatile("ld.global.nc.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
+    asm volatile("ld.global.nc.b32 %0, [%1];\n" : "=r"(w[0]) : "l"(p));
+  }
+}
+
+template <int D, bool F8>
+struct Shape {
+  static constexpr int kRow = F8 ? D : 2 * D;                    // bytes of a row
+  static constexpr int kKVec = (kRow / 4) % 16 == 0 ? 16 : 8;    // bytes of a K piece
+  static constexpr int kVVec = (kRow / 8) % 16 == 0 ? 16 : ((kRow / 8) % 8 == 0 ? 8 : 4);
+  static constexpr int kKWords = kRow / 16, kVWords = kRow / 32;  // words a lane has of a row
+  static constexpr int kElt = F8 ? 1 : 2;
+  // the dimension of element e of the lane's part of a K or V row
+  __device__ static int k_dim(int e, int t) {
+    constexpr int v = kKVec / kElt;
+    return (e / v) * 4 * v + t * v + e % v;
+  }
+  __device__ static int v_dim(int e, int g) {
+    constexpr int v = kVVec / kElt;
+    return (e / v) * 8 * v + g * v + e % v;
+  }
+};
+
+template <int D, bool F8>
+struct Tile {
+  uint32_t k[2][Shape<D, F8>::kKWords];
+  uint32_t v[4][Shape<D, F8>::kVWords];
+  float k_scale, v_scale;
+  int key0;  // first key; -1: nothing there
+};
+
+template <int D, bool F8>
+__device__ __forceinline__ void load_tile(const KvAttnParams &a, int s, int head, int key0, int lane,
+                                          Tile<D, F8> &x) {
+  using S = Shape<D, F8>;
+  const int g = lane >> 2, t = lane & 3;
+  const int at = (int)((unsigned)key0 / (unsigned)a.b.page_tokens);
+  const int page = kv_page(a.b, s, at);
+  x.key0 = page < 0 ? -1 : key0;
+  if (page < 0) return;
+  const int slot = key0 - at * a.b.page_tokens;
+  const int64_t h = (int64_t)page * a.b.h_kv + head;
+  const int64_t off = (h * a.b.page_tokens + slot) * S::kRow;
+  const uint8_t *kp = static_cast<const uint8_t *>(a.ck) + off;
+  const uint8_t *vp = static_cast<const uint8_t *>(a.cv) + off;
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int j = 0; j < S::kKWords * 4 / S::kKVec; ++j)
+      load_bytes<S::kKVec>(kp + (g + 8 * r) * S::kRow + (j * 4 + t) * S::kKVec,
+                           &x.k[r][j * S::kKVec / 4]);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int j = 0; j < S::kVWords * 4 / S::kVVec; ++j)
+      load_bytes<S::kVVec>(vp + (2 * t + (r & 1) + 8 * (r >> 1)) * S::kRow + (j * 8 + g) * S::kVVec,
+                           &x.v[r][j * S::kVVec / 4]);
+  if constexpr (F8) {
+    const int64_t b = h * (a.b.page_tokens / kKvBlock) + slot / kKvBlock;
+    x.k_scale = exp2i(kv_scale_exp(__ldg(a.k_scale + b)));
+    x.v_scale = exp2i(kv_scale_exp(__ldg(a.v_scale + b)));
+  }
+}
+
+// O^T += V^T P^T for one 16-key tile; with PART only into this lane's columns
+// that `mine` names.
+template <int D, bool F8, int TERMS, bool PART>
+__device__ __forceinline__ void add_pv(float (&o)[D / 16][4], const uint32_t (&v)[4][Shape<D, F8>::kVWords],
+                                       float v_scale, const uint32_t (&p0)[TERMS],
+                                       const uint32_t (&p1)[TERMS], const bool (&mine)[2]) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    uint32_t f[4];
+    if constexpr (F8) {
+      const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
+      const uint32_t lo = __byte_perm(v[0][i / 2], v[1][i / 2], sel);
+      const uint32_t hi = __byte_perm(v[2][i / 2], v[3][i / 2], sel);
+      f[0] = e4m3_half2(lo);
+      f[1] = e4m3_half2(lo >> 16);
+      f[2] = e4m3_half2(hi);
+      f[3] = e4m3_half2(hi >> 16);
+    } else {
+      f[0] = __byte_perm(v[0][i], v[1][i], 0x5410);
+      f[1] = __byte_perm(v[0][i], v[1][i], 0x7632);
+      f[2] = __byte_perm(v[2][i], v[3][i], 0x5410);
+      f[3] = __byte_perm(v[2][i], v[3][i], 0x7632);
+    }
+    if constexpr (F8 || PART) {
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < TERMS; ++u) mma16<F8>(c, f, p0[u], p1[u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!PART || mine[e & 1]) o[i][e] = fmaf(c[e], F8 ? v_scale : 1.0f, o[i][e]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < TERMS; ++u) mma16<F8>(o[i], f, p0[u], p1[u]);
+    }
+  }
+}
+
+template <int D, bool F8, int TERMS>
+__global__ void __launch_bounds__(kThreads) kv_attention_kernel(KvAttnParams a) {
+  using S = Shape<D, F8>;
+  constexpr int kSteps = D / 16;
+  constexpr float kShift = F8 ? 15.0f : 0.0f;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (blockIdx.x == gridDim.x - 1) {
+    write_status(a);
+    return;
+  }
+  __shared__ float s_m[kWarps][kCols], s_l[kWarps][kCols];
+  __shared__ float s_o[kWarps][kCols][D + 4];
+  int x = blockIdx.x;
+  const int split = x % a.splits;
+  x /= a.splits;
+  const int ct = x % a.col_tiles;
+  x /= a.col_tiles;
+  const int head = x % a.b.h_kv, s = x / a.b.h_kv;
+  const KvSeq q = kv_seq(a.b, s);
+  const int c0 = ct * kCols, c1 = min(c0 + kCols, q.rows * a.G);  // columns of this block
+  if (c0 >= c1) return;
+  const int first = q.len - q.rows;  // position of the sequence's first row
+  const int p_lo = first + c0 / a.G, p_hi = first + (c1 - 1) / a.G;
+  const KvTiles tiles = visible_tiles(a, p_lo, p_hi);
+  const int i0 = split * a.tiles_per_split, i1 = min(i0 + a.tiles_per_split, tiles.count);
+  if (split > 0 && i0 >= tiles.count) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+  // q's fragments: column g, this lane's dimensions
+  uint32_t qf[TERMS][kSteps][2];
+  float col_scale;  // of column g: softmax scale * log2 e, and q's power of two back
+  {
+    const int c = c0 + g;
+    float qv[4 * kSteps];
+    float big = 0.0f;
+    const int row = q.row0 + c / a.G, h = head * a.G + c % a.G;
+#pragma unroll
+    for (int e = 0; e < 4 * kSteps; ++e) {
+      qv[e] = c < c1 ? load_q(a.q, a.q_bf16, (int64_t)row * a.q_stride + (int64_t)h * D + S::k_dim(e, t))
+                     : 0.0f;
+      big = fmaxf(big, fabsf(qv[e]));
+    }
+    col_scale = a.qscale;
+    if constexpr (F8) {
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // big to [2^14, 2^15): exact, and 28 binades below stay normal
+      const int e = min(max(14 - (((__float_as_int(big) >> 23) & 255) - 127), -120), 120);
+      const float f = exp2i(e);
+#pragma unroll
+      for (int i = 0; i < 4 * kSteps; ++i) qv[i] *= f;
+      col_scale *= exp2i(-e);
+    }
+#pragma unroll
+    for (int u = 0; u < TERMS; ++u)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          qf[u][i][w] = split16<F8>(qv[4 * i + 2 * w], qv[4 * i + 2 * w + 1]);
+  }
+  // of this lane's accumulator columns 2t and 2t + 1: scale and position
+  float cs[2];
+  int pc[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    cs[j] = __shfl_sync(0xffffffffu, col_scale, 4 * (2 * t + j));
+    pc[j] = first + min(c0 + 2 * t + j, c1 - 1) / a.G;
+  }
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  float o[D / 16][4];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+
+  auto fold = [&](const Tile<D, F8> &x) {
+    if (x.key0 < 0) return;
+    float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      uint32_t f[4];
+      if constexpr (F8) {
+        f[0] = e4m3_half2(x.k[0][i]);
+        f[1] = e4m3_half2(x.k[1][i]);
+        f[2] = e4m3_half2(x.k[0][i] >> 16);
+        f[3] = e4m3_half2(x.k[1][i] >> 16);
+      } else {
+        f[0] = x.k[0][2 * i];
+        f[1] = x.k[1][2 * i];
+        f[2] = x.k[0][2 * i + 1];
+        f[3] = x.k[1][2 * i + 1];
+      }
+#pragma unroll
+      for (int u = 0; u < TERMS; ++u) mma16<F8>(sc, f, qf[u][i][0], qf[u][i][1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[e] *= F8 ? cs[e & 1] * x.k_scale : cs[e & 1];
+    const bool whole = x.key0 + kKvBlock - 1 <= p_lo &&
+                       (x.key0 + kKvBlock <= a.sinks || x.key0 > p_hi - a.window);
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!sees(a, pc[e & 1], x.key0 + g + 8 * (e >> 1))) sc[e] = -INFINITY;
+    }
+    float corr[2];
+    float mn[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float b = fmaxf(sc[j], sc[j + 2]);
+      b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 4));
+      b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 8));
+      b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 16));
+      mn[j] = fmaxf(m[j], b);
+    }
+    if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        corr[j] = mn[j] == -INFINITY ? 1.0f : exp2f(m[j] - mn[j]);
+        l[j] *= corr[j];
+        m[j] = mn[j];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= corr[e & 1];
+    }
+    float p[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float ref = m[e & 1] == -INFINITY ? 0.0f : m[e & 1] - kShift;
+      p[e] = exp2f(sc[e] - ref);
+      l[e & 1] += p[e];
+    }
+    uint32_t p0[TERMS], p1[TERMS];
+#pragma unroll
+    for (int u = 0; u < TERMS; ++u) {
+      p0[u] = transpose8(split16<F8>(p[0], p[1]));
+      p1[u] = transpose8(split16<F8>(p[2], p[3]));
+    }
+    if (whole) {
+      add_pv<D, F8, TERMS, false>(o, x.v, x.v_scale, p0, p1, {true, true});
+      return;
+    }
+    // token by token: V rows that the token does not see become zeros, and only
+    // its columns take the product
+    for (int pos = p_lo; pos <= p_hi; ++pos) {
+      uint32_t v[4][S::kVWords];
+      const bool mine[2] = {pc[0] == pos, pc[1] == pos};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool see = sees(a, pos, x.key0 + 2 * t + (r & 1) + 8 * (r >> 1));
+#pragma unroll
+        for (int w = 0; w < S::kVWords; ++w) v[r][w] = see ? x.v[r][w] : 0u;
+      }
+      add_pv<D, F8, TERMS, true>(o, v, x.v_scale, p0, p1, mine);
+    }
+  };
+
+  auto key_of = [&](int i) { return kKvBlock * (i < tiles.sink_tiles ? i : i + tiles.skip); };
+  // two tiles in flight: the next one's loads are issued before the current one
+  // is worked on
+  Tile<D, F8> ta, tb;
+  int i = i0 + warp;
+  if (i < i1) load_tile<D, F8>(a, s, head, key_of(i), lane, ta);
+  while (i < i1) {
+    if (i + kWarps < i1) load_tile<D, F8>(a, s, head, key_of(i + kWarps), lane, tb);
+    fold(ta);
+    i += kWarps;
+    if (i >= i1) break;
+    if (i + kWarps < i1) load_tile<D, F8>(a, s, head, key_of(i + kWarps), lane, ta);
+    fold(tb);
+    i += kWarps;
+  }
+
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
+    if (g == 0) {
+      s_m[warp][2 * t + j] = m[j];
+      s_l[warp][2 * t + j] = l[j];
+    }
+  }
+#pragma unroll
+  for (int i2 = 0; i2 < D / 16; ++i2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s_o[warp][2 * t + (e & 1)][S::v_dim(2 * i2 + (e >> 1), g)] = o[i2][e];
+  __syncthreads();
+  for (int y = threadIdx.x; y < (c1 - c0) * D; y += kThreads) {
+    const int c = y / D, dim = y % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][c]);
+    float L = 0.0f, O = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = s_m[w][c] == -INFINITY ? 0.0f : exp2f(s_m[w][c] - M);
+      L = fmaf(s_l[w][c], f, L);
+      // (a warp that saw nothing has zeros)
+      O = fmaf(s_o[w][c][dim], f, O);
+    }
+    const int row = q.row0 + (c0 + c) / a.G, h = head * a.G + (c0 + c) % a.G;
+    const int64_t rh = (int64_t)row * a.h_q + h;
+    if (a.splits == 1) {
+      store_out(a, rh * D + dim, L > 0.0f ? O / L : (L == 0.0f ? 0.0f : L));
+      if (dim == 0 && a.lse) a.lse[rh] = lse_of(M, L, kShift);
+    } else {
+      const int64_t part = (int64_t)split * a.b.num_rows * a.h_q + rh;
+      a.part_o[part * D + dim] = O;
+      if (dim == 0) a.part_ml[part] = make_float2(M, L);
+    }
+  }
+}
+
+// Joins the splits of one (row, head): a warp each.
+__global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, int d, float shift) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t rh = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (rh >= (int64_t)a.b.num_rows * a.h_q) return;
+  const int row = (int)(rh / a.h_q), h = (int)(rh % a.h_q);
+  const int s = a.b.q_start ? find_seq(a.b.num_seqs, row, [&](int i) { return a.b.q_start[i]; }) : row;
+  const KvSeq q = kv_seq(a.b, s);
+  if (row < q.row0 || row >= q.row0 + q.rows) return;
+  const int col = (row - q.row0) * a.G + h % a.G, c0 = col / kCols * kCols;
+  const int c1 = min(c0 + kCols, q.rows * a.G), first = q.len - q.rows;
+  const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G);
+  const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
+  const int64_t step = (int64_t)a.b.num_rows * a.h_q;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[i * step + rh].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float L = 0.0f, o[FATHOM_MAX_D / 32];
+#pragma unroll
+  for (int j = 0; j < FATHOM_MAX_D / 32; ++j) o[j] = 0.0f;
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = a.part_ml[i * step + rh];
+    const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+    L = fmaf(ml.y, f, L);
+    const float *po = a.part_o + (i * step + rh) * d;
+#pragma unroll
+    for (int j = 0; j < FATHOM_MAX_D / 32; ++j)
+      if (32 * j < d) o[j] = fmaf(po[32 * j + lane], f, o[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < FATHOM_MAX_D / 32; ++j)
+    if (32 * j < d)
+      store_out(a, rh * d + 32 * j + lane, L > 0.0f ? o[j] / L : (L == 0.0f ? 0.0f : L));
+  if (lane == 0 && a.lse) a.lse[rh] = lse_of(M, L, shift);
+}
+
+template <int D>
+cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
+  const int64_t blocks = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles * a.splits + 1;
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  cudaError_t e;
+  if (f8)
+    e = a.q_bf16 ? launch_dependent(kv_attention_kernel<D, true, 1>, grid, block, 0, s, a)
+                 : launch_dependent(kv_attention_kernel<D, true, 2>, grid, block, 0, s, a);
+  else
+    e = a.q_bf16 ? launch_dependent(kv_attention_kernel<D, false, 1>, grid, block, 0, s, a)
+                 : launch_dependent(kv_attention_kernel<D, false, 3>, grid, block, 0, s, a);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const int64_t rh = (int64_t)a.b.num_rows * a.h_q;
+  return launch_dependent(kv_combine_kernel, dim3((unsigned)((rh + kWarps - 1) / kWarps)), block, 0,
+                          s, a, D, f8 ? 15.0f : 0.0f);
+}
+
+}  // namespace
+
+void plan_kv_attention(KvAttnParams &a) {
+  a.col_tiles = (int)(((int64_t)a.b.max_rows * a.G + kCols - 1) / kCols);
+  // the most tiles that one block's columns can see
+  const int64_t tokens = (kCols + a.G - 2) / a.G + 1;  // tokens that 8 columns can span
+  int64_t most = ((int64_t)a.b.max_len + kKvBlock - 1) / kKvBlock;
+  if (a.window < a.b.max_len) {
+    const int64_t w = ((int64_t)a.window + tokens - 1 + kKvBlock - 2) / kKvBlock + 1 +
+                      ((int64_t)a.sinks + kKvBlock - 1) / kKvBlock;
+    if (w < most) most = w;
+  }
+  if (most < 1) most = 1;
+  // enough blocks for every SM to hold several, and at least 4 tiles a warp
+  const int64_t base = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles;
+  const int64_t want = (8 * 148 + base - 1) / base;
+  int64_t splits = most / (4 * kWarps);
+  if (splits > want) splits = want;
+  if (splits < 1) splits = 1;
+  a.tiles_per_split = (int)((most + splits - 1) / splits);
+  a.splits = (int)((most + a.tiles_per_split - 1) / a.tiles_per_split);
+}
+
+cudaError_t launch_kv_attention(const KvAttnParams &a, int d, bool f8, cudaStream_t s) {
+  switch (d / 32) {
+    case 1: return launch_d<32>(a, f8, s);
+    case 2: return launch_d<64>(a, f8, s);
+    case 3: return launch_d<96>(a, f8, s);
+    case 4: return launch_d<128>(a, f8, s);
+    case 5: return launch_d<160>(a, f8, s);
+    case 6: return launch_d<192>(a, f8, s);
+    case 7: return launch_d<224>(a, f8, s);
+    case 8: return launch_d<256>(a, f8, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fathom

@@ -1,0 +1,82 @@
+// Attention over the paged cache: parameters and what its kernels share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv_cache.cuh"
+
+namespace fathom {
+
+struct KvAttnParams {
+  KvBatch b;
+  const void *ck, *cv;
+  const uint8_t *k_scale, *v_scale;
+  const void *q;
+  int64_t q_stride;
+  int q_bf16;  // and out's type
+  int h_q, G;
+  float qscale;       // softmax scale * log2(e)
+  int window, sinks;  // window: above max_len where there is none
+  void *out;
+  float *lse;
+  // the plan (plan_kv_attention) and the workspace
+  int col_tiles, tiles_per_split, splits;
+  WsStatus *status;
+  float2 *part_ml;  // [splits][num_rows * h_q]: maximum (log2 units), sum
+  float *part_o;    // [splits][num_rows * h_q][d]
+};
+
+// Whether a row at position p sees token j.
+__device__ __forceinline__ bool sees(const KvAttnParams &a, int p, int j) {
+  return j <= p && (j > p - a.window || j < a.sinks);
+}
+
+// The 16-key tiles that rows at positions p_lo .. p_hi can see: those of the
+// first `sinks` tokens, then, `skip` tiles further on, the windows'.
+struct KvTiles {
+  int count, sink_tiles, skip;
+};
+
+__device__ __forceinline__ KvTiles visible_tiles(const KvAttnParams &a, int p_lo, int p_hi) {
+  KvTiles x;
+  const int end = p_hi < 0 ? 0 : p_hi / kKvBlock + 1;
+  const int from = max(p_lo - a.window + 1, 0) / kKvBlock;
+  const int sink = (int)min(((int64_t)a.sinks + kKvBlock - 1) / kKvBlock, (int64_t)end);
+  x.sink_tiles = min(sink, from);
+  x.skip = from - x.sink_tiles;
+  x.count = max(end - x.skip, 0);
+  return x;
+}
+
+__device__ __forceinline__ void store_out(const KvAttnParams &a, int64_t at, float x) {
+  if (a.q_bf16)
+    static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(x);
+  else
+    static_cast<float *>(a.out)[at] = x;
+}
+
+// log of the sum of exp(s), from the sum l of 2^(s' - m + shift), s' = s log2 e.
+__device__ __forceinline__ float lse_of(float m, float l, float shift) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l) - shift) * 0.6931471805599453f;
+}
+
+// The last block of a launch counts the sequences that break the batch's
+// bounds into the workspace's status.
+__device__ __forceinline__ void write_status(const KvAttnParams &a) {
+  __shared__ int bad;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  int n = 0;
+  for (int s = threadIdx.x; s < a.b.num_seqs; s += blockDim.x) n += !kv_seq(a.b, s).valid;
+  if (n) atomicAdd(&bad, n);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.status->fallback_heads = 0;
+    a.status->device_faults = (uint32_t)bad;
+    a.status->max_candidates = 0;
+    a.status->union_planes = 0;
+  }
+}
+
+}  // namespace fathom

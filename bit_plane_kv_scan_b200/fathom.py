@@ -31,6 +31,7 @@ ERR_DEVICE_CHECK = 5
 
 F32 = 0
 BF16 = 1
+E4M3 = 2
 PLANES_DEVICE = 0
 PLANES_HOST_MAPPED = 1
 FLAG_NO_SAMPLING = 1
@@ -45,11 +46,16 @@ EXPORTED = [
     "fathom_scan_topk_batched_workspace_size", "fathom_scan_topk_batched",
     "fathom_scan_read_report", "fathom_profile_scan_kernel", "fathom_scan_topk_noalloc",
     "fathom_scan_read_report_noalloc", "fathom_check_device_status", "fathom_merge_topk",
-    "fathom_sparse_attention",
+    "fathom_sparse_attention", "fathom_kv_append", "fathom_kv_attention_workspace_size",
+    "fathom_kv_attention",
 ]
 NOALLOC_SCRATCH_BYTES = 16 << 20
 TOKEN_GROUP_QUANTUM = 65536
 MAX_MERGE_PARTS = 64
+KV_BLOCK = 16
+KV_SCALE_MIN = 8
+KV_SCALE_MAX = 246
+KV_MAX_LEN = 1 << 30
 
 
 class FathomError(RuntimeError):
@@ -100,6 +106,44 @@ class BatchedArgs(ctypes.Structure):
     ]
 
 
+class KvCacheArgs(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("page_tokens", ctypes.c_int), ("h_kv", ctypes.c_int), ("d", ctypes.c_int),
+    ]
+
+
+class KvBatchArgs(ctypes.Structure):
+    _fields_ = [
+        ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p), ("num_seqs", ctypes.c_int), ("table_width", ctypes.c_int),
+        ("num_rows", ctypes.c_int), ("max_rows", ctypes.c_int), ("max_len", ctypes.c_int64),
+    ]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", KvCacheArgs), ("batch", KvBatchArgs),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kv_dtype", ctypes.c_int),
+        ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_dtype", ctypes.c_int),
+        ("h_q", ctypes.c_int), ("q_stride", ctypes.c_int64),
+        ("inv_freq", ctypes.c_void_p), ("rotary_pairs", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+    ]
+
+
+class KvAttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", KvCacheArgs), ("batch", KvBatchArgs),
+        ("q", ctypes.c_void_p), ("q_dtype", ctypes.c_int), ("h_q", ctypes.c_int),
+        ("q_stride", ctypes.c_int64), ("softmax_scale", ctypes.c_float),
+        ("window", ctypes.c_int64), ("sinks", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
 class ScanReport(ctypes.Structure):
     _fields_ = [("fallback_heads", ctypes.c_uint32), ("device_faults", ctypes.c_uint32),
                 ("max_candidates", ctypes.c_uint32), ("union_planes", ctypes.c_uint32)]
@@ -135,6 +179,12 @@ def lib() -> ctypes.CDLL:
         L.fathom_allocate_uniform.argtypes = [ci, ci, ci, vp, vp]
         L.fathom_sparse_attention.restype = ci
         L.fathom_sparse_attention.argtypes = [ctypes.POINTER(AttentionArgs), vp]
+        L.fathom_kv_append.restype = ci
+        L.fathom_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), vp]
+        L.fathom_kv_attention_workspace_size.restype = sz
+        L.fathom_kv_attention_workspace_size.argtypes = [ctypes.POINTER(KvAttentionArgs)]
+        L.fathom_kv_attention.restype = ci
+        L.fathom_kv_attention.argtypes = [ctypes.POINTER(KvAttentionArgs), vp, sz, vp]
         L.fathom_scan_topk_workspace_size.restype = sz
         L.fathom_scan_topk_workspace_size.argtypes = [ctypes.POINTER(ScanArgs)]
         L.fathom_scan_topk.restype = ci
@@ -506,3 +556,208 @@ def check_device_status(workspace: Optional[Workspace] = None, device=None, stre
     ws = _workspace(workspace, device or "cuda")
     _check(lib().fathom_check_device_status(_ptr(ws.buf[(-ws.buf.data_ptr()) % 256:]),
                                             _stream(stream)))
+
+
+class KVCache:
+    """A layer's paged cache of keys and values.
+
+    k, v [num_pages, h_kv, page_tokens, d], bfloat16 or float8_e4m3fn, contiguous;
+    page_tokens a multiple of KV_BLOCK.  With float8_e4m3fn, k_scale and v_scale
+    uint8 [num_pages, h_kv, page_tokens / KV_BLOCK] hold each block's scale as an
+    exponent byte x: an element stands for code * 2^(x - 127)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None):
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise TypeError("k and v must both be bfloat16 or both float8_e4m3fn")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [num_pages, h_kv, page_tokens, d]")
+        pages, h_kv, tokens, d = k.shape
+        if tokens % KV_BLOCK:
+            raise ValueError("page_tokens must be a multiple of %d" % KV_BLOCK)
+        tensors = [k, v]
+        if k.dtype == torch.float8_e4m3fn:
+            for x in (k_scale, v_scale):
+                if x is None or x.dtype != torch.uint8:
+                    raise TypeError("a float8_e4m3fn cache needs uint8 k_scale and v_scale")
+                if tuple(x.shape) != (pages, h_kv, tokens // KV_BLOCK):
+                    raise ValueError("scales must be [num_pages, h_kv, page_tokens / %d]" % KV_BLOCK)
+            tensors += [k_scale, v_scale]
+        elif k_scale is not None or v_scale is not None:
+            raise TypeError("a bfloat16 cache has no scales")
+        _same_device(*tensors)
+        if not all(x.is_contiguous() for x in tensors):
+            raise ValueError("the cache's tensors must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.args = KvCacheArgs(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
+                                dtype=BF16 if k.dtype == torch.bfloat16 else E4M3, num_pages=pages,
+                                page_tokens=tokens, h_kv=h_kv, d=d)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_tokens: int, h_kv: int, d: int,
+              dtype: torch.dtype = torch.bfloat16, device=None) -> "KVCache":
+        """A cache of zeros."""
+        device = torch.device(device or "cuda")
+        shape = (num_pages, h_kv, page_tokens, d)
+        if dtype == torch.bfloat16:
+            return cls(torch.zeros(shape, dtype=dtype, device=device),
+                       torch.zeros(shape, dtype=dtype, device=device))
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+        return cls(k, v, *(torch.full((num_pages, h_kv, page_tokens // KV_BLOCK), KV_SCALE_MIN,
+                                      dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+class KVBatch:
+    """The sequences of one step and their new tokens (rows).
+
+    page_table int32 [num_seqs, width]; seq_len int32 [num_seqs], the tokens of
+    each sequence with its rows counted; q_start int32 [num_seqs + 1], where
+    sequence s has rows q_start[s] .. q_start[s + 1] - 1 (None: one row each).
+    All on the GPU, read there only; num_rows, max_rows and max_len are the host's
+    bounds on them (defaults: one row each; the tokens that the table can hold).
+    The tensors may be rewritten in place between calls and graph replays."""
+
+    def __init__(self, page_table: torch.Tensor, seq_len: torch.Tensor,
+                 q_start: Optional[torch.Tensor] = None, *, num_rows: Optional[int] = None,
+                 max_rows: Optional[int] = None, max_len: Optional[int] = None):
+        tensors = [page_table, seq_len] + ([] if q_start is None else [q_start])
+        if any(x.dtype != torch.int32 for x in tensors):
+            raise TypeError("page_table, seq_len and q_start must be int32")
+        if page_table.dim() != 2 or tuple(seq_len.shape) != (page_table.shape[0],):
+            raise ValueError("page_table must be [num_seqs, width] and seq_len [num_seqs]")
+        seqs = page_table.shape[0]
+        if q_start is not None and tuple(q_start.shape) != (seqs + 1,):
+            raise ValueError("q_start must be [num_seqs + 1]")
+        if q_start is not None and num_rows is None:
+            raise ValueError("q_start needs num_rows")
+        if not all(x.is_contiguous() for x in tensors):
+            raise ValueError("the batch's tensors must be contiguous")
+        _same_device(*tensors)
+        rows = seqs if num_rows is None else int(num_rows)
+        if max_rows is None:
+            max_rows = rows if q_start is not None else min(1, rows)
+        self.page_table, self.seq_len, self.q_start = page_table, seq_len, q_start
+        self.num_rows, self.max_rows, self.max_len = rows, int(max_rows), max_len
+        self.device = page_table.device
+
+    def args_for(self, cache: KVCache) -> KvBatchArgs:
+        most = self.max_len
+        if most is None:
+            most = min(self.page_table.shape[1] * cache.args.page_tokens, KV_MAX_LEN)
+        return KvBatchArgs(page_table=_ptr(self.page_table), seq_len=_ptr(self.seq_len),
+                           q_start=_ptr(self.q_start), num_seqs=self.page_table.shape[0],
+                           table_width=self.page_table.shape[1], num_rows=self.num_rows,
+                           max_rows=self.max_rows, max_len=int(most))
+
+
+def _same_device(*tensors: torch.Tensor) -> torch.device:
+    device = tensors[0].device
+    for x in tensors[1:]:
+        if x.device != device:
+            raise ValueError("tensors on %s and %s" % (device, x.device))
+    return device
+
+
+def _rows_of(x: torch.Tensor, name: str, rows: int, d: int) -> int:
+    """The row stride of [rows, heads, d] rows whose heads are contiguous."""
+    if x.dim() != 3 or x.shape[0] != rows or x.shape[2] != d:
+        raise ValueError("%s must be [num_rows=%d, heads, d=%d]" % (name, rows, d))
+    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d)):
+        raise ValueError("%s: each row's heads must be contiguous" % name)
+    return x.stride(0) if rows > 1 else 0
+
+
+def _launch_stream(stream, device: torch.device):
+    return torch.cuda.current_stream(device) if stream is None else stream
+
+
+def _hold(stream, device: torch.device, *tensors):
+    """Memory that torch allocated for its current stream but that `stream` uses:
+    the allocator must not hand it out again before `stream` has passed."""
+    if stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
+        for x in tensors:
+            if x is not None:
+                x.record_stream(stream)
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, *,
+              q: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+              interleaved: bool = False, q_out: Optional[torch.Tensor] = None, stream=None):
+    """Put the rows' keys and values [num_rows, h_kv, d] (bf16/f32) into the cache,
+    keys and queries rotated by their positions.
+
+    inv_freq float32 [pairs]: pair r of a row at position p turns by p * inv_freq[r]
+    (None: no rotation); pair r is dimensions r and r + pairs, or 2r and 2r + 1 with
+    interleaved.  Rows may be strided (parts of a fused projection).  Returns the
+    rotated q [num_rows, h_q, d] (None without q); q_out=q rotates in place."""
+    c = cache.args
+    _same_device(cache.k, batch.page_table, k, v, *(x for x in (q, inv_freq, q_out) if x is not None))
+    ks, vs = _rows_of(k, "k", batch.num_rows, c.d), _rows_of(v, "v", batch.num_rows, c.d)
+    if k.shape[1] != c.h_kv or v.shape[1] != c.h_kv or v.dtype != k.dtype:
+        raise ValueError("k and v must both be [num_rows, h_kv=%d, d] of one dtype" % c.h_kv)
+    pairs = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise TypeError("inv_freq must be a contiguous float32 [pairs] tensor")
+        pairs = inv_freq.shape[0]
+    a = KvAppendArgs(cache=c, batch=batch.args_for(cache), k=_ptr(k), v=_ptr(v),
+                     kv_dtype=_dtype_code(k), k_stride=ks, v_stride=vs,
+                     inv_freq=_ptr(inv_freq) if pairs else None, rotary_pairs=pairs,
+                     interleaved=int(interleaved))
+    with torch.cuda.device(cache.device):
+        stream = _launch_stream(stream, cache.device)
+        if q is not None:
+            a.q_stride = _rows_of(q, "q", batch.num_rows, c.d)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                _hold(stream, cache.device, q_out)
+            elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+                raise ValueError("q_out must be contiguous, of q's shape and dtype")
+            a.q, a.q_out, a.q_dtype, a.h_q = _ptr(q), _ptr(q_out), _dtype_code(q), q.shape[1]
+        _check(lib().fathom_kv_append(ctypes.byref(a), ctypes.c_void_p(stream.cuda_stream)))
+    return q_out if q is not None else None
+
+
+def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
+                 softmax_scale: Optional[float] = None, *, window: int = 0, sinks: int = 0,
+                 workspace: Optional[Workspace] = None, stream=None,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """Attention of the rows q [num_rows, h_q, d] (bf16/f32) over their sequences'
+    cache: every token up to the row's own, or with window > 0 the last `window` of
+    them and the first `sinks`.
+
+    Returns (out [num_rows, h_q, d] of q's dtype, lse f32 [num_rows, h_q]); rows that
+    no sequence has are left as they were.  Without a workspace the call takes
+    one from torch's allocator, so that two captured graphs never share one."""
+    c = cache.args
+    _same_device(cache.k, batch.page_table, q, *(x for x in (out, lse) if x is not None))
+    qs = _rows_of(q, "q", batch.num_rows, c.d)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / float(c.d) ** 0.5
+    a = KvAttentionArgs(cache=c, batch=batch.args_for(cache), q=_ptr(q), q_dtype=_dtype_code(q),
+                        h_q=q.shape[1], q_stride=qs, softmax_scale=float(softmax_scale),
+                        window=int(window), sinks=int(sinks))
+    L = lib()
+    with torch.cuda.device(cache.device):
+        stream = _launch_stream(stream, cache.device)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _hold(stream, cache.device, out)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of q's shape and dtype")
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+            _hold(stream, cache.device, lse)
+        elif lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 [num_rows, h_q]")
+        a.out, a.lse = _ptr(out), _ptr(lse)
+        need = L.fathom_kv_attention_workspace_size(ctypes.byref(a))
+        if workspace is None:
+            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
+            _hold(stream, cache.device, ws)
+        else:
+            ws = workspace.get(need)
+        _check(L.fathom_kv_attention(ctypes.byref(a), _ptr(ws), need,
+                                     ctypes.c_void_p(stream.cuda_stream)))
+    return out, lse

@@ -30,6 +30,13 @@
  *                        callers that cannot allocate;
  *   fathom_scan_read_report, fathom_check_device_status    what the last
  *                        scan on a workspace recorded (faults, fallbacks).
+ * Beside it, the paged cache that holds a layer's keys and values as they are
+ * decoded (bf16, or 8-bit with a scale per block of tokens and head):
+ *   fathom_kv_append           rotates new keys (and queries) by their
+ *                        positions and puts keys and values into the pages;
+ *   fathom_kv_attention        new tokens' attention over every earlier token,
+ *                        or over a sliding window and a few first tokens: the
+ *                        layers and contexts that are not read sparsely.
  * fathom_scan_args.token_group selects the quantiser variant with (m, s) per
  * run of token_group keys instead of per channel over the whole context.
  *
@@ -78,7 +85,9 @@ typedef enum fathom_status {
   FATHOM_ERR_DEVICE_CHECK = 5          /* a device-side check recorded a fault */
 } fathom_status;
 
-typedef enum fathom_dtype { FATHOM_F32 = 0, FATHOM_BF16 = 1 } fathom_dtype;
+/* FATHOM_E4M3 (8-bit float, 4 exponent and 3 mantissa bits, largest 448) is a
+ * paged cache's element type only (fathom_kv_cache). */
+typedef enum fathom_dtype { FATHOM_F32 = 0, FATHOM_BF16 = 1, FATHOM_E4M3 = 2 } fathom_dtype;
 
 typedef enum fathom_planes_location {
   FATHOM_PLANES_DEVICE = 0,      /* planes in device memory (HBM) */
@@ -408,6 +417,152 @@ typedef struct fathom_attention_args {
 } fathom_attention_args;
 
 FATHOM_API fathom_status fathom_sparse_attention(const fathom_attention_args *args, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged KV cache.  The paper has no counterpart: it scans a cache that a
+ * serving stack holds; these calls fill such a cache and read it densely,
+ * where a layer is not read sparsely (a prompt, a windowed layer, a short
+ * context).
+ *
+ * One layer's keys and values, in pages of page_tokens tokens that sequences
+ * take in any order:
+ *   k, v   [num_pages][h_kv][page_tokens][d] of dtype FATHOM_BF16 or
+ *          FATHOM_E4M3, 16-byte aligned;
+ *   k_scale, v_scale   with FATHOM_E4M3, uint8
+ *          [num_pages][h_kv][page_tokens / FATHOM_KV_BLOCK]: the scale of each
+ *          block of 16 tokens of one KV head, a power of two held as its
+ *          exponent byte x.  An element stands for code * 2^(x - 127), which
+ *          is exact in bf16.  FATHOM_KV_SCALE_MIN <= x <= FATHOM_KV_SCALE_MAX;
+ *          a byte outside is read as the nearer bound.
+ * Token j of sequence s is row j % page_tokens of page
+ * page_table[s][j / page_tokens].  A page that is a whole context
+ * (num_pages = 1, FATHOM_BF16) is the [h_kv][n][d] layout which
+ * fathom_sparse_attention gathers from.
+ * Requires d as FATHOM_MAX_D, page_tokens a positive multiple of
+ * FATHOM_KV_BLOCK up to 2^30, num_pages >= 1 and h_kv >= 1.
+ */
+#define FATHOM_KV_BLOCK 16
+#define FATHOM_KV_SCALE_MIN 8
+#define FATHOM_KV_SCALE_MAX 246
+#define FATHOM_KV_MAX_LEN (1 << 30) /* tokens of a sequence */
+
+typedef struct fathom_kv_cache {
+  void *k;
+  void *v;
+  uint8_t *k_scale;  /* FATHOM_E4M3 only, else NULL */
+  uint8_t *v_scale;
+  int dtype;         /* FATHOM_BF16 or FATHOM_E4M3 */
+  int num_pages, page_tokens, h_kv, d;
+} fathom_kv_cache;
+
+/* The sequences of one step and their new tokens (rows), packed one sequence
+ * behind the other.  The arrays are DEVICE memory which the host never reads,
+ * so a captured graph may be replayed with other contents:
+ *   page_table [num_seqs][table_width]: pages of each sequence, in order;
+ *   seq_len    [num_seqs]: tokens of each sequence, its new rows included;
+ *   q_start    [num_seqs + 1]: sequence s has rows q_start[s] ..
+ *              q_start[s + 1] - 1, its last tokens: row i of m has position
+ *              seq_len[s] - m + i.  NULL: num_rows == num_seqs, one row each.
+ * Host bounds, from which launches and workspaces are sized: num_rows rows in
+ * all, at most max_rows of one sequence, no sequence longer than max_len.
+ * The kernels check the arrays against the bounds: a sequence with seq_len < 0
+ * or > max_len counts as empty, one whose rows are not within [0, num_rows) or
+ * number more than max_rows as having no rows, and a page outside
+ * [0, num_pages) or beyond table_width as holding nothing: its tokens are
+ * neither written nor seen. */
+typedef struct fathom_kv_batch {
+  const int32_t *page_table;
+  const int32_t *seq_len;
+  const int32_t *q_start;
+  int num_seqs, table_width, num_rows, max_rows;
+  int64_t max_len;  /* 0 <= max_len <= FATHOM_KV_MAX_LEN */
+} fathom_kv_batch;
+
+/* fathom_kv_append -- puts the rows' keys and values into the cache, keys (and
+ * queries) rotated by their positions on the way.
+ *   k, v     [num_rows][h_kv][d] of kv_dtype (FATHOM_BF16 or FATHOM_F32), rows
+ *            k_stride / v_stride elements apart (0: h_kv * d), e.g. parts of a
+ *            fused projection's output.
+ *   inv_freq [rotary_pairs] float, or NULL (rotary_pairs = 0) for no rotation.
+ *            Pair r of a row at position p turns by the angle p * inv_freq[r],
+ *            formed in 64 bits: (x, y) -> (x cos - y sin, y cos + x sin).  Pair
+ *            r is dimensions r and r + rotary_pairs, or with interleaved set
+ *            2 r and 2 r + 1; dimensions from 2 * rotary_pairs on stay.
+ *   q        optional [num_rows][h_q][d] of q_dtype (FATHOM_BF16 or
+ *            FATHOM_F32), rows q_stride elements apart (0: h_q * d); rotated
+ *            into q_out [num_rows][h_q][d], which may be q itself where
+ *            q_stride is h_q * d, and otherwise must not overlap it.
+ * FATHOM_BF16 cache: each element rounded once.  FATHOM_E4M3 cache: a block's
+ * scale is the smallest power of two with max |x| <= 256 * scale over the
+ * block's new finite elements as they came (turning a pair grows an element by
+ * sqrt 2 at most, and 256 sqrt 2 < 448), and no smaller than the scale of the
+ * tokens that the sequence already had in that block, whose codes move to it
+ * (rounded to nearest even, as the new ones are).  Larger elements than a code
+ * can hold saturate; a NaN stays a NaN.
+ * A row at a negative position (seq_len below the sequence's rows) is not
+ * written; rows that no sequence has are left alone.  Two sequences of one call, or two
+ * calls that overlap, must not append to the same block (shared pages are for
+ * reading).
+ */
+typedef struct fathom_kv_append_args {
+  fathom_kv_cache cache;
+  fathom_kv_batch batch;
+  const void *k;
+  const void *v;
+  int kv_dtype;
+  int64_t k_stride, v_stride;
+  const void *q;
+  void *q_out;
+  int q_dtype;
+  int h_q;
+  int64_t q_stride;
+  const float *inv_freq;
+  int rotary_pairs;  /* 0 <= 2 * rotary_pairs <= d */
+  int interleaved;
+} fathom_kv_append_args;
+
+FATHOM_API fathom_status fathom_kv_append(const fathom_kv_append_args *args, void *stream);
+
+/* fathom_kv_attention -- attention of the rows over their own sequences' cache.
+ * Row at position p, query head h (KV head g = h / G) sees token j when
+ *   j <= p and (window == 0 or j > p - window or j < sinks):
+ * every token up to its own, or the last `window` of them (its own included)
+ * and the first `sinks`.
+ *   s_j = softmax_scale * <q[h], k_j>,
+ *   out[h] = sum_j softmax(s)_j v_j,   lse[h] = log(sum_j exp(s_j)).
+ * A row that sees nothing gets out = 0 and lse = -inf.  What a token that a row
+ * does not see holds (a NaN, an infinity) does not reach that row.
+ *   q    [num_rows][h_q][d] of q_dtype (FATHOM_BF16 or FATHOM_F32), rows
+ *        q_stride elements apart (0: h_q * d).
+ *   out  [num_rows][h_q][d] of q_dtype; lse float [num_rows][h_q] or NULL.
+ *        Rows that no sequence has are left as they were.
+ * Products run on the tensor cores with sums, maxima and softmax statistics in
+ * fp32.  FATHOM_BF16 queries: softmax weights are rounded to 16 bits before they
+ * meet V.  FATHOM_F32 queries and their weights are split into 16-bit terms
+ * that keep 22 bits or more.
+ * Requires h_q a multiple of h_kv, a finite softmax_scale, window >= 0 and
+ * sinks >= 0.  The workspace (fathom_kv_attention_workspace_size bytes, 0 on
+ * bad arguments) is 256-byte aligned device memory, which the call need not
+ * find cleared; calls sharing one must not overlap.  It starts with the status
+ * that fathom_check_device_status reads: a sequence that the batch's bounds
+ * reject is a device fault.
+ */
+typedef struct fathom_kv_attention_args {
+  fathom_kv_cache cache;
+  fathom_kv_batch batch;
+  const void *q;
+  int q_dtype;
+  int h_q;
+  int64_t q_stride;
+  float softmax_scale;
+  int64_t window, sinks;
+  void *out;
+  float *lse;
+} fathom_kv_attention_args;
+
+FATHOM_API size_t fathom_kv_attention_workspace_size(const fathom_kv_attention_args *args);
+FATHOM_API fathom_status fathom_kv_attention(const fathom_kv_attention_args *args, void *workspace,
+                                             size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
