@@ -33,8 +33,6 @@ cudaError_t launch_merge_parts(const int32_t *in_idx, const float *in_score, int
                                float *out_score, cudaStream_t stream);
 int tc_plan_bytes(int d);
 cudaError_t launch_kv_append(const fathom_kv_append_args *a, const KvBatch &b, cudaStream_t stream);
-void plan_kv_attention(KvAttnParams &a);
-cudaError_t launch_kv_attention(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
 }  // namespace fathom
 
 using namespace fathom;
@@ -288,7 +286,7 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   if ((int64_t)a->batch.max_rows * p.G > FATHOM_KV_MAX_LEN)
     return fail(FATHOM_ERR_UNSUPPORTED, "max_rows=%d times %d heads a KV head is too many",
                 a->batch.max_rows, p.G);
-  plan_kv_attention(p);
+  plan_kv_attention(p, a->cache.d);
   if ((double)p.b.num_seqs * p.b.h_kv * p.col_tiles * p.splits >= 2147483647.0)
     return fail(FATHOM_ERR_UNSUPPORTED,
                 "num_seqs=%d max_rows=%d h_q=%d: too many blocks for one launch", p.b.num_seqs,
@@ -296,11 +294,21 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   return FATHOM_OK;
 }
 
-// The workspace: status, then the splits' maxima and sums, then their outputs.
-size_t kv_workspace(const KvAttnParams &p, int d, size_t *off_o) {
+// The workspace: status, the units' marks, then the splits' maxima and sums and
+// their outputs.
+struct KvWorkspace {
+  size_t off_taint, off_ml, off_o, total;
+};
+
+KvWorkspace kv_workspace(const KvAttnParams &p, int d) {
   const size_t parts = p.splits > 1 ? (size_t)p.splits * p.b.num_rows * p.h_q : 0;
-  *off_o = sizeof(WsStatus) + up256(parts * 8);
-  return *off_o + up256(parts * d * 4);
+  const size_t marks = p.many_rows ? (size_t)p.b.num_seqs * p.b.h_kv * p.col_tiles * p.splits : 0;
+  KvWorkspace w;
+  w.off_taint = sizeof(WsStatus);
+  w.off_ml = w.off_taint + up256(marks * 4);
+  w.off_o = w.off_ml + up256(parts * 8);
+  w.total = w.off_o + up256(parts * d * 4);
+  return w;
 }
 
 }  // namespace
@@ -691,8 +699,7 @@ fathom_status fathom_kv_append(const fathom_kv_append_args *a, void *stream) {
 size_t fathom_kv_attention_workspace_size(const fathom_kv_attention_args *a) {
   KvAttnParams p;
   if (check_kv_attention(a, p) != FATHOM_OK) return 0;
-  size_t off_o;
-  return kv_workspace(p, a->cache.d, &off_o);
+  return kv_workspace(p, a->cache.d).total;
 }
 
 fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, size_t ws_bytes,
@@ -709,10 +716,10 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   REQUIRE_ON_DEVICE(a->out, "out", el);
   if (a->lse) REQUIRE_ON_DEVICE(a->lse, "lse", 4);
   REQUIRE_ON_DEVICE(ws, "workspace", 256);
-  size_t off_o;
-  const size_t need = kv_workspace(p, a->cache.d, &off_o);
-  if (ws_bytes < need)
-    return fail(FATHOM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  const KvWorkspace w = kv_workspace(p, a->cache.d);
+  if (ws_bytes < w.total)
+    return fail(FATHOM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes,
+                w.total);
   p.ck = a->cache.k;
   p.cv = a->cache.v;
   p.k_scale = a->cache.k_scale;
@@ -722,8 +729,9 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   p.lse = a->lse;
   unsigned char *base = static_cast<unsigned char *>(ws);
   p.status = reinterpret_cast<WsStatus *>(base);
-  p.part_ml = reinterpret_cast<float2 *>(base + sizeof(WsStatus));
-  p.part_o = reinterpret_cast<float *>(base + off_o);
+  p.taint = reinterpret_cast<int *>(base + w.off_taint);
+  p.part_ml = reinterpret_cast<float2 *>(base + w.off_ml);
+  p.part_o = reinterpret_cast<float *>(base + w.off_o);
   cudaError_t e = launch_kv_attention(p, a->cache.d, a->cache.dtype == FATHOM_E4M3,
                                       (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");

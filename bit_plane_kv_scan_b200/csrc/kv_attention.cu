@@ -204,31 +204,21 @@ __device__ __forceinline__ void add_pv(float (&o)[D / 16][4], const uint32_t (&v
   }
 }
 
+// One thread block's share: column tile ct of sequence s and KV head `head`, the
+// split-th run of its keys.
 template <int D, bool F8, int TERMS>
-__global__ void __launch_bounds__(kThreads) kv_attention_kernel(KvAttnParams a) {
+__device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, int ct, int split) {
   using S = Shape<D, F8>;
   constexpr int kSteps = D / 16;
   constexpr float kShift = F8 ? 15.0f : 0.0f;
-  grid_dependency_wait();
-  allow_dependent_launch();
-  if (blockIdx.x == gridDim.x - 1) {
-    write_status(a);
-    return;
-  }
   __shared__ float s_m[kWarps][kCols], s_l[kWarps][kCols];
   __shared__ float s_o[kWarps][kCols][D + 4];
-  int x = blockIdx.x;
-  const int split = x % a.splits;
-  x /= a.splits;
-  const int ct = x % a.col_tiles;
-  x /= a.col_tiles;
-  const int head = x % a.b.h_kv, s = x / a.b.h_kv;
   const KvSeq q = kv_seq(a.b, s);
   const int c0 = ct * kCols, c1 = min(c0 + kCols, q.rows * a.G);  // columns of this block
   if (c0 >= c1) return;
   const int first = q.len - q.rows;  // position of the sequence's first row
   const int p_lo = first + c0 / a.G, p_hi = first + (c1 - 1) / a.G;
-  const KvTiles tiles = visible_tiles(a, p_lo, p_hi);
+  const KvTiles tiles = visible_tiles(a, p_lo, p_hi, kKvBlock);
   const int i0 = split * a.tiles_per_split, i1 = min(i0 + a.tiles_per_split, tiles.count);
   if (split > 0 && i0 >= tiles.count) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -304,8 +294,7 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(KvAttnParams a) 
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) sc[e] *= F8 ? cs[e & 1] * x.k_scale : cs[e & 1];
-    const bool whole = x.key0 + kKvBlock - 1 <= p_lo &&
-                       (x.key0 + kKvBlock <= a.sinks || x.key0 > p_hi - a.window);
+    const bool whole = sees_all(a, p_lo, p_hi, x.key0, kKvBlock);
     if (!whole) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -365,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(KvAttnParams a) 
     }
   };
 
-  auto key_of = [&](int i) { return kKvBlock * (i < tiles.sink_tiles ? i : i + tiles.skip); };
+  auto key_of = [&](int i) { return kKvBlock * tiles.at(i); };
   // two tiles in flight: the next one's loads are issued before the current one
   // is worked on
   Tile<D, F8> ta, tb;
@@ -423,6 +412,44 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(KvAttnParams a) 
   }
 }
 
+template <int D, bool F8, int TERMS>
+__global__ void __launch_bounds__(kThreads) kv_attention_kernel(KvAttnParams a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (blockIdx.x == gridDim.x - 1) {
+    write_status(a);
+    return;
+  }
+  int x = blockIdx.x;
+  const int split = x % a.splits;
+  x /= a.splits;
+  const int ct = x % a.col_tiles;
+  x /= a.col_tiles;
+  attend<D, F8, TERMS>(a, x / a.b.h_kv, x % a.b.h_kv, ct, split);
+}
+
+// After the many-rows kernel: the units that it marked, column tile by column
+// tile, each over all its keys.
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int per = a.cols / kCols, units = a.b.num_seqs * a.b.h_kv * a.col_tiles;
+  KvAttnParams b = a;
+  b.splits = 1;
+  b.tiles_per_split = 1 << 30;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    int marked = 0;
+    for (int i = threadIdx.x; i < a.splits; i += kThreads) marked |= a.taint[(int64_t)u * a.splits + i];
+    if (!__syncthreads_or(marked)) continue;
+    const int rb = u % a.col_tiles, x = u / a.col_tiles;
+    for (int ct = 0; ct < per; ++ct) {
+      attend<D, F8, 1>(b, x / b.b.h_kv, x % b.b.h_kv, rb * per + ct, 0);
+      __syncthreads();
+    }
+  }
+}
+
 // Joins the splits of one (row, head): a warp each.
 __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, int d, float shift) {
   grid_dependency_wait();
@@ -434,9 +461,9 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, in
   const int s = a.b.q_start ? find_seq(a.b.num_seqs, row, [&](int i) { return a.b.q_start[i]; }) : row;
   const KvSeq q = kv_seq(a.b, s);
   if (row < q.row0 || row >= q.row0 + q.rows) return;
-  const int col = (row - q.row0) * a.G + h % a.G, c0 = col / kCols * kCols;
-  const int c1 = min(c0 + kCols, q.rows * a.G), first = q.len - q.rows;
-  const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G);
+  const int col = (row - q.row0) * a.G + h % a.G, c0 = col / a.cols * a.cols;
+  const int c1 = min(c0 + a.cols, q.rows * a.G), first = q.len - q.rows;
+  const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
   const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
   const int64_t step = (int64_t)a.b.num_rows * a.h_q;
   float M = -INFINITY;
@@ -462,41 +489,67 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, in
   if (lane == 0 && a.lse) a.lse[rh] = lse_of(M, L, shift);
 }
 
+template <int D, bool F8>
+cudaError_t launch_redo(const KvAttnParams &a, cudaStream_t s) {
+  const int units = a.b.num_seqs * a.b.h_kv * a.col_tiles;
+  return launch_dependent(kv_redo_kernel<D, F8>, dim3(units < 444 ? units : 444), dim3(kThreads), 0,
+                          s, a);
+}
+
 template <int D>
 cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
   const int64_t blocks = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles * a.splits + 1;
   const dim3 grid((unsigned)blocks), block(kThreads);
   cudaError_t e;
-  if (f8)
+  if (a.many_rows)
+    e = launch_kv_prompt(a, D, f8, s);
+  else if (f8)
     e = a.q_bf16 ? launch_dependent(kv_attention_kernel<D, true, 1>, grid, block, 0, s, a)
                  : launch_dependent(kv_attention_kernel<D, true, 2>, grid, block, 0, s, a);
   else
     e = a.q_bf16 ? launch_dependent(kv_attention_kernel<D, false, 1>, grid, block, 0, s, a)
                  : launch_dependent(kv_attention_kernel<D, false, 3>, grid, block, 0, s, a);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  const int64_t rh = (int64_t)a.b.num_rows * a.h_q;
-  return launch_dependent(kv_combine_kernel, dim3((unsigned)((rh + kWarps - 1) / kWarps)), block, 0,
-                          s, a, D, f8 ? 15.0f : 0.0f);
+  if (e == cudaSuccess && a.splits > 1) {
+    const int64_t rh = (int64_t)a.b.num_rows * a.h_q;
+    e = launch_dependent(kv_combine_kernel, dim3((unsigned)((rh + kWarps - 1) / kWarps)), block, 0,
+                         s, a, D, f8 && !a.many_rows ? 15.0f : 0.0f);
+  }
+  if constexpr (D == 64 || D == 128)
+    if (e == cudaSuccess && a.many_rows)
+      e = f8 ? launch_redo<D, true>(a, s) : launch_redo<D, false>(a, s);
+  return e;
 }
 
 }  // namespace
 
-void plan_kv_attention(KvAttnParams &a) {
-  a.col_tiles = (int)(((int64_t)a.b.max_rows * a.G + kCols - 1) / kCols);
-  // the most tiles that one block's columns can see
-  const int64_t tokens = (kCols + a.G - 2) / a.G + 1;  // tokens that 8 columns can span
-  int64_t most = ((int64_t)a.b.max_len + kKvBlock - 1) / kKvBlock;
+void plan_kv_attention(KvAttnParams &a, int d) {
+  // The tcgen05 kernel multiplies 256 columns at a time: it takes over where
+  // sequences have 64 columns or more and the queries are bf16.
+  a.many_rows = a.q_bf16 && (d == 64 || d == 128) && (int64_t)a.b.max_rows * a.G >= 64;
+  a.cols = a.many_rows ? kPromptCols : kCols;
+  a.tile = a.many_rows ? kPromptTile : kKvBlock;
+  a.col_tiles = (int)(((int64_t)a.b.max_rows * a.G + a.cols - 1) / a.cols);
+  // the most tiles that one unit's columns can see
+  const int64_t tokens = (a.cols + a.G - 2) / a.G + 1;  // tokens that `cols` columns can span
+  int64_t most = ((int64_t)a.b.max_len + a.tile - 1) / a.tile;
   if (a.window < a.b.max_len) {
-    const int64_t w = ((int64_t)a.window + tokens - 1 + kKvBlock - 2) / kKvBlock + 1 +
-                      ((int64_t)a.sinks + kKvBlock - 1) / kKvBlock;
+    const int64_t w = ((int64_t)a.window + tokens - 1 + a.tile - 2) / a.tile + 1 +
+                      ((int64_t)a.sinks + a.tile - 1) / a.tile;
     if (w < most) most = w;
   }
   if (most < 1) most = 1;
-  // enough blocks for every SM to hold several, and at least 4 tiles a warp
   const int64_t base = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles;
-  const int64_t want = (8 * 148 + base - 1) / base;
-  int64_t splits = most / (4 * kWarps);
-  if (splits > want) splits = want;
+  int64_t splits;
+  if (a.many_rows) {
+    // one block an SM, and at least 8 tiles a block
+    splits = 148 / base;
+    if (splits > most / 8) splits = most / 8;
+  } else {
+    // enough blocks for every SM to hold several, and at least 4 tiles a warp
+    const int64_t want = (8 * 148 + base - 1) / base;
+    splits = most / (4 * kWarps);
+    if (splits > want) splits = want;
+  }
   if (splits < 1) splits = 1;
   a.tiles_per_split = (int)((most + splits - 1) / splits);
   a.splits = (int)((most + a.tiles_per_split - 1) / a.tiles_per_split);

@@ -8,6 +8,10 @@
 
 namespace fathom {
 
+// The many-rows kernel's unit: two tiles of 128 columns, against 128 keys at a time.
+constexpr int kPromptCols = 256;
+constexpr int kPromptTile = 128;
+
 struct KvAttnParams {
   KvBatch b;
   const void *ck, *cv;
@@ -20,9 +24,14 @@ struct KvAttnParams {
   int window, sinks;  // window: above max_len where there is none
   void *out;
   float *lse;
-  // the plan (plan_kv_attention) and the workspace
+  // The plan (plan_kv_attention) and the workspace.  A unit of work is `cols`
+  // (token, head) pairs of one sequence and KV head; it goes through its keys in
+  // tiles of `tile`, divided over `splits` thread blocks.
+  int many_rows;  // the tcgen05 kernel
+  int cols, tile;
   int col_tiles, tiles_per_split, splits;
   WsStatus *status;
+  int *taint;       // many_rows: [units][splits], see kv_prompt.cu
   float2 *part_ml;  // [splits][num_rows * h_q]: maximum (log2 units), sum
   float *part_o;    // [splits][num_rows * h_q][d]
 };
@@ -32,21 +41,29 @@ __device__ __forceinline__ bool sees(const KvAttnParams &a, int p, int j) {
   return j <= p && (j > p - a.window || j < a.sinks);
 }
 
-// The 16-key tiles that rows at positions p_lo .. p_hi can see: those of the
-// first `sinks` tokens, then, `skip` tiles further on, the windows'.
+// The tiles of `tile` keys that rows at positions p_lo .. p_hi can see: those of
+// the first `sinks` tokens, then, `skip` tiles further on, the windows'.
 struct KvTiles {
   int count, sink_tiles, skip;
+  __device__ __forceinline__ int at(int i) const { return i < sink_tiles ? i : i + skip; }
 };
 
-__device__ __forceinline__ KvTiles visible_tiles(const KvAttnParams &a, int p_lo, int p_hi) {
+__device__ __forceinline__ KvTiles visible_tiles(const KvAttnParams &a, int p_lo, int p_hi,
+                                                 int tile) {
   KvTiles x;
-  const int end = p_hi < 0 ? 0 : p_hi / kKvBlock + 1;
-  const int from = max(p_lo - a.window + 1, 0) / kKvBlock;
-  const int sink = (int)min(((int64_t)a.sinks + kKvBlock - 1) / kKvBlock, (int64_t)end);
+  const int end = p_hi < 0 ? 0 : p_hi / tile + 1;
+  const int from = max(p_lo - a.window + 1, 0) / tile;
+  const int sink = (int)min(((int64_t)a.sinks + tile - 1) / tile, (int64_t)end);
   x.sink_tiles = min(sink, from);
   x.skip = from - x.sink_tiles;
   x.count = max(end - x.skip, 0);
   return x;
+}
+
+// Whether every row at positions p_lo .. p_hi sees all of key0 .. key0 + tile - 1.
+__device__ __forceinline__ bool sees_all(const KvAttnParams &a, int p_lo, int p_hi, int key0,
+                                         int tile) {
+  return key0 + tile - 1 <= p_lo && (key0 + tile <= a.sinks || key0 > p_hi - a.window);
 }
 
 __device__ __forceinline__ void store_out(const KvAttnParams &a, int64_t at, float x) {
@@ -78,5 +95,11 @@ __device__ __forceinline__ void write_status(const KvAttnParams &a) {
     a.status->union_planes = 0;
   }
 }
+
+// kv_attention.cu
+cudaError_t launch_kv_attention(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
+void plan_kv_attention(KvAttnParams &a, int d);
+// kv_prompt.cu: the tcgen05 kernel alone
+cudaError_t launch_kv_prompt(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
 
 }  // namespace fathom
