@@ -18,7 +18,8 @@
 //
 // Warps: 0-3 and 4-7 the softmax of the two tiles; 8-11 load Q, K and V into
 // shared memory, by cp.async (bf16) or through registers (e4m3, which becomes
-// bf16 exactly, its power-of-two scale included); 12 issues the MMAs.  K and V go
+// bf16 exactly, its power-of-two scale included); 12 issues the MMAs (13-15 are
+// there to give up their registers).  K and V go
 // through a ring of 4 buffers in 128-byte swizzled rows; pages may be as small as
 // 16 tokens.  Keys that no row of the unit sees, and those on bad pages, arrive as
 // zeros.
@@ -39,7 +40,12 @@ namespace {
 constexpr int kSoftWarps = 8;  // 4 for each tile
 constexpr int kLoadWarp0 = kSoftWarps, kLoadWarps = 4;
 constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);  // 416
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // 512: the MMA warp's group has no other work
+// Registers: 512 threads are launched with 128 each, 65536 in all.  The softmax
+// keeps a row of 128 scores in registers; the other groups give theirs up:
+// 256 * 192 + 128 * 88 + 128 * 40 = 65536.
+constexpr int kSoftRegs = 192, kLoadRegs = 88, kMmaRegs = 40;
+static_assert(kSoftRegs * 256 + (kLoadRegs + kMmaRegs) * 128 <= 65536, "registers of the block");
 constexpr int kLoadThreads = 32 * kLoadWarps;
 constexpr int kM = 128;                  // rows of a tile
 constexpr int kN = kPromptTile;          // keys of a tile
@@ -93,6 +99,44 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 
 __device__ __forceinline__ void proxy_fence() {
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// 2^x, results below 2^-126 to 0 (hardware; off by 2^-22 of the value).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations in one.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // mbar_wait with one answer for the whole (converged) warp.
@@ -222,10 +266,165 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
   auto t_s = [&](int i) { return tmem + kN * i; };
   auto t_o = [&](int i) { return tmem + 2 * kN + D * i; };
 
-  if (nt <= 0) {
-    // no row sees anything: the epilogue below writes zeros
-  } else if (warp >= kLoadWarp0 && warp < kMmaWarp) {
+  if (warp < kSoftWarps) {
+    // ----------------------------------------------------------- softmax --
+    regs_up<kSoftRegs>();
+    const int m = warp / 4, r = tid % kM;  // tile and row
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int c = c0 + m * kM + r;
+    const int pos = first + min(c, c1 - 1) / a.G;
+    const float cs = fmaxf(fabsf(a.qscale), 1e-37f);  // (0 would make NaN of a masked score)
+    float ref = -INFINITY, l = 0.0f;
+    bool live = true;
+    if (nt > 0 && m < n_m) {
+      const int t_lo = first + (c0 + m * kM) / a.G;
+      const int t_hi = first + (min(c0 + m * kM + kM, c1) - 1) / a.G;
+      // blocks of 16 keys that are there, of tile j
+      auto blocks_of = [&](int j) {
+        const int key = kN * tiles.at(i0 + j) + kKvBlock * (lane & 7);
+        const bool ok = key < q.len &&
+                        kv_page(a.b, s, (int)((unsigned)key / (unsigned)a.b.page_tokens)) >= 0;
+        return __ballot_sync(0xffffffffu, ok) & 0xffu;
+      };
+      uint32_t blocks = blocks_of(0);
+      for (int j = 0; j < nt; ++j) {
+        const int key0 = kN * tiles.at(i0 + j);
+        const uint32_t here = blocks;
+        if (j + 1 < nt) blocks = blocks_of(j + 1);
+        const bool whole = here == 0xffu && sees_all(a, t_lo, t_hi, key0, kN);
+        // the keys that this row sees, of 32 from key0 + 32 i
+        auto seen = [&](int i) {
+          const int k0 = key0 + 32 * i;
+          uint32_t b = low_bits(pos - k0 + 1) &
+                       (~low_bits(pos - a.window + 1 - k0) | low_bits(a.sinks - k0));
+          if (!(here >> (2 * i) & 1)) b &= 0xffff0000u;
+          if (!(here >> (2 * i + 1) & 1)) b &= 0x0000ffffu;
+          return b;
+        };
+        if (!warp_wait(s_full(m), j & 1)) {
+          live = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[kN / 32][32];
+#pragma unroll
+        for (int i = 0; i < kN / 32; ++i) tc_ld32(t_s(m) + lanes + 32 * i, v[i]);
+        tc_wait_ld();
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < kN / 32; ++i) {
+            const uint32_t see = seen(i);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1)) v[i][e] = 0xff800000u;  // -inf
+          }
+        }
+        float top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top[i] = __uint_as_float(v[i][0]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2)
+            top[i] = fmaxf(top[i], fmaxf(__uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1])));
+          top[i] = fmaxf(top[i], __uint_as_float(v[i][31]));
+        }
+        float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        mx = mx == -INFINITY ? mx : mx * cs;
+        const bool grow = mx > ref + kSlack;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float next = grow ? mx : ref;
+          const float f = ref == next ? 1.0f : exp2f(ref - next);
+          l *= f;
+          ref = next;
+          if (j > 0) {  // (tile 0 overwrites O)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tc_ld16(t_o(m) + lanes + 16 * i, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc_st16(t_o(m) + lanes + 16 * i, o);
+            }
+          }
+        }
+        const float sub = ref == -INFINITY ? 0.0f : ref;
+        const uint64_t cs2 = pack2(cs, cs), sub2 = pack2(-sub, -sub);
+        uint64_t sum = 0ull, sum2 = 0ull;
+#pragma unroll
+        for (int i = 0; i < kN / 32; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint32_t *x = &v[i][e];
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), cs2, sub2));
+            const float p0 = ex2(y.x), p1 = ex2(y.y);
+            if (e & 2)
+              sum2 = add2(sum2, pack2(p0, p1));
+            else
+              sum = add2(sum, pack2(p0, p1));
+            w[e / 2] = bf16x2(p0, p1);
+          }
+          tc_st16(t_s(m) + lanes + 16 * i, w);
+        }
+        const float2 part = unpack2(add2(sum, sum2));
+        l += part.x + part.y;
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full(m));
+      }
+      if (live) live = warp_wait(o_full, 0);
+      if (!live) s_fault = 1;
+      tc_fence_after();
+    }
+    // ---------------------------------------------------------- epilogue --
+    if (m < n_m && live) {
+      const int row = q.row0 + c / a.G, h = head * a.G + c % a.G;
+      const int64_t rh = (int64_t)row * a.h_q + h;
+      const bool mine = c < c1;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      const int64_t part = (int64_t)split * a.b.num_rows * a.h_q + rh;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0u;
+        if (nt > 0) {
+          tc_ld32(t_o(m) + lanes + 32 * i, v);
+          tc_wait_ld();
+        }
+        if (!mine) continue;
+        if (a.splits == 1) {
+          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + rh * D + 32 * i;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float x0 = l == 0.0f ? 0.0f : __uint_as_float(v[e]) * inv;
+            const float x1 = l == 0.0f ? 0.0f : __uint_as_float(v[e + 1]) * inv;
+            reinterpret_cast<__nv_bfloat162 *>(out)[e / 2] = __floats2bfloat162_rn(x0, x1);
+          }
+        } else {
+          float *out = a.part_o + part * D + 32 * i;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(out + e) =
+                l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                          : make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                        __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+        }
+      }
+      if (mine) {
+        if (a.splits == 1) {
+          if (a.lse) a.lse[rh] = lse_of(ref, l, 0.0f);
+        } else {
+          a.part_ml[part] = make_float2(ref, l);
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------- loads --
+    // (nt = 0: no row sees anything; the softmax warps write zeros)
+    regs_down<kLoadRegs>();
+    if (nt > 0) {
     const int t = tid - 32 * kLoadWarp0;
     {  // Q: rows c0 .. c1 - 1, the rest zeros; its sign makes c >= 0
       constexpr int kChunks = D / 8;  // 16-byte pieces of a row
@@ -389,8 +588,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
         for (int i = 0; i < kIter; ++i) w[i] = next[i];
       }
     }
-  } else if (warp == kMmaWarp) {
+    }
+  } else {
     // -------------------------------------------------------------- MMAs --
+    regs_down<kMmaRegs>();
+    if (warp == kMmaWarp && nt > 0) {
     constexpr uint32_t kIdS = idesc(kN, false), kIdO = idesc(D, true);
     const bool leader = tc_elect_one();
     bool live = mbar_wait(q_full, 0);
@@ -444,162 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
     }
     commit(o_full);
     if (!live) s_fault = 1;
-  }
-  if (warp < kSoftWarps) {
-    // ----------------------------------------------------------- softmax --
-    const int m = warp / 4, r = tid % kM;  // tile and row
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const int c = c0 + m * kM + r;
-    const int pos = first + min(c, c1 - 1) / a.G;
-    const float cs = fmaxf(fabsf(a.qscale), 1e-37f);  // (0 would make NaN of a masked score)
-    float ref = -INFINITY, l = 0.0f;
-    bool live = true;
-    if (nt > 0 && m < n_m) {
-      const int t_lo = first + (c0 + m * kM) / a.G;
-      const int t_hi = first + (min(c0 + m * kM + kM, c1) - 1) / a.G;
-      // blocks of 16 keys that are there, of tile j
-      auto blocks_of = [&](int j) {
-        const int key = kN * tiles.at(i0 + j) + kKvBlock * (lane & 7);
-        const bool ok = key < q.len &&
-                        kv_page(a.b, s, (int)((unsigned)key / (unsigned)a.b.page_tokens)) >= 0;
-        return __ballot_sync(0xffffffffu, ok) & 0xffu;
-      };
-      uint32_t blocks = blocks_of(0);
-      for (int j = 0; j < nt; ++j) {
-        const int key0 = kN * tiles.at(i0 + j);
-        const uint32_t here = blocks;
-        if (j + 1 < nt) blocks = blocks_of(j + 1);
-        const bool whole = here == 0xffu && sees_all(a, t_lo, t_hi, key0, kN);
-        // the keys that this row sees, of 32 from key0 + 32 i
-        auto seen = [&](int i) {
-          const int k0 = key0 + 32 * i;
-          uint32_t b = low_bits(pos - k0 + 1) &
-                       (~low_bits(pos - a.window + 1 - k0) | low_bits(a.sinks - k0));
-          if (!(here >> (2 * i) & 1)) b &= 0xffff0000u;
-          if (!(here >> (2 * i + 1) & 1)) b &= 0x0000ffffu;
-          return b;
-        };
-        if (!warp_wait(s_full(m), j & 1)) {
-          live = false;
-          break;
-        }
-        tc_fence_after();
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kN / 32; ++i) {
-          uint32_t v[32];
-          tc_ld32(t_s(m) + lanes + 32 * i, v);
-          tc_wait_ld();
-          if (whole) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
-          } else {
-            const uint32_t see = seen(i);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              mx = fmaxf(mx, see >> e & 1 ? __uint_as_float(v[e]) : -INFINITY);
-          }
-        }
-        mx = mx == -INFINITY ? mx : mx * cs;
-        const bool grow = mx > ref + kSlack;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float next = grow ? mx : ref;
-          const float f = ref == next ? 1.0f : exp2f(ref - next);
-          l *= f;
-          ref = next;
-          if (j > 0) {  // (tile 0 overwrites O)
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t v[32];
-              tc_ld32(t_o(m) + lanes + 32 * i, v);
-              tc_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-              tc_st32(t_o(m) + lanes + 32 * i, v);
-            }
-          }
-        }
-        const float sub = ref == -INFINITY ? 0.0f : ref;
-        float l2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kN / 64; ++i) {
-          uint32_t w[32];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t v[32];
-            tc_ld32(t_s(m) + lanes + 64 * i + 32 * half, v);
-            tc_wait_ld();
-            if (!whole) {
-              const uint32_t see = seen(2 * i + half);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(see >> e & 1)) v[e] = 0xff800000u;  // -inf
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float p0 = exp2f(fmaf(__uint_as_float(v[e]), cs, -sub));
-              const float p1 = exp2f(fmaf(__uint_as_float(v[e + 1]), cs, -sub));
-              l += p0;
-              l2 += p1;
-              w[16 * half + e / 2] = bf16x2(p0, p1);
-            }
-          }
-          tc_st32(t_s(m) + lanes + 32 * i, w);
-        }
-        l += l2;
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(p_full(m));
-      }
-      if (live) live = warp_wait(o_full, 0);
-      if (!live) s_fault = 1;
-      tc_fence_after();
-    }
-    // ---------------------------------------------------------- epilogue --
-    if (m < n_m && live) {
-      const int row = q.row0 + c / a.G, h = head * a.G + c % a.G;
-      const int64_t rh = (int64_t)row * a.h_q + h;
-      const bool mine = c < c1;
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-      const int64_t part = (int64_t)split * a.b.num_rows * a.h_q + rh;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0u;
-        if (nt > 0) {
-          tc_ld32(t_o(m) + lanes + 32 * i, v);
-          tc_wait_ld();
-        }
-        if (!mine) continue;
-        if (a.splits == 1) {
-          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + rh * D + 32 * i;
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float x0 = l == 0.0f ? 0.0f : __uint_as_float(v[e]) * inv;
-            const float x1 = l == 0.0f ? 0.0f : __uint_as_float(v[e + 1]) * inv;
-            reinterpret_cast<__nv_bfloat162 *>(out)[e / 2] = __floats2bfloat162_rn(x0, x1);
-          }
-        } else {
-          float *out = a.part_o + part * D + 32 * i;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(out + e) =
-                l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                          : make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
-                                        __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-        }
-      }
-      if (mine) {
-        if (a.splits == 1) {
-          if (a.lse) a.lse[rh] = lse_of(ref, l, 0.0f);
-        } else {
-          a.part_ml[part] = make_float2(ref, l);
-        }
-      }
     }
   }
-
   // Every MMA is complete once o_full has arrived; then the ring's last commits
   // are waited for, so that no arrival is pending when the barriers go away.
   tc_fence_before();
