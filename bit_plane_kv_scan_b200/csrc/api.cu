@@ -286,7 +286,7 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   if ((int64_t)a->batch.max_rows * p.G > FATHOM_KV_MAX_LEN)
     return fail(FATHOM_ERR_UNSUPPORTED, "max_rows=%d times %d heads a KV head is too many",
                 a->batch.max_rows, p.G);
-  plan_kv_attention(p, a->cache.d);
+  plan_kv_attention(p, a->cache.d, a->cache.dtype == FATHOM_E4M3);
   if ((double)p.b.num_seqs * p.b.h_kv * p.col_tiles * p.splits >= 2147483647.0)
     return fail(FATHOM_ERR_UNSUPPORTED,
                 "num_seqs=%d max_rows=%d h_q=%d: too many blocks for one launch", p.b.num_seqs,
@@ -294,10 +294,10 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   return FATHOM_OK;
 }
 
-// The workspace: status, the units' marks, then the splits' maxima and sums and
-// their outputs.
+// The workspace: status, the units' marks, the splits' maxima and sums and their
+// outputs, then the widened keys and values.
 struct KvWorkspace {
-  size_t off_taint, off_ml, off_o, total;
+  size_t off_taint, off_ml, off_o, off_wide, total;
 };
 
 KvWorkspace kv_workspace(const KvAttnParams &p, int d) {
@@ -307,7 +307,8 @@ KvWorkspace kv_workspace(const KvAttnParams &p, int d) {
   w.off_taint = sizeof(WsStatus);
   w.off_ml = w.off_taint + up256(marks * 4);
   w.off_o = w.off_ml + up256(parts * 8);
-  w.total = w.off_o + up256(parts * d * 4);
+  w.off_wide = w.off_o + up256(parts * d * 4);
+  w.total = w.off_wide + (size_t)(p.many_rows ? p.pairs : 0) * p.n_pad * d * 4;
   return w;
 }
 
@@ -732,6 +733,7 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   p.taint = reinterpret_cast<int *>(base + w.off_taint);
   p.part_ml = reinterpret_cast<float2 *>(base + w.off_ml);
   p.part_o = reinterpret_cast<float *>(base + w.off_o);
+  p.wide = reinterpret_cast<const uint16_t *>(base + w.off_wide);
   cudaError_t e = launch_kv_attention(p, a->cache.d, a->cache.dtype == FATHOM_E4M3,
                                       (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");

@@ -522,10 +522,27 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
 
 }  // namespace
 
-void plan_kv_attention(KvAttnParams &a, int d) {
+void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
   // The tcgen05 kernel multiplies 256 columns at a time: it takes over where
-  // sequences have 64 columns or more and the queries are bf16.
-  a.many_rows = a.q_bf16 && (d == 64 || d == 128) && (int64_t)a.b.max_rows * a.G >= 64;
+  // sequences have 64 columns or more and the queries are bf16.  (Its tensor map
+  // counts the cache's rows in 31 bits.)
+  const int64_t rows = (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
+  a.many_rows = a.q_bf16 && (d == 64 || d == 128) && (int64_t)a.b.max_rows * a.G >= 64 &&
+                (f8 || rows < ((int64_t)1 << 31));
+  const int64_t all_pairs = (int64_t)a.b.num_seqs * a.b.h_kv;
+  a.pair0 = 0;
+  a.pairs = (int)all_pairs;
+  a.n_pad = 0;
+  a.box_rows = kPromptTile;
+  if (a.many_rows && f8) {
+    // The widened copy holds as many pairs at a time as fit in 1 GiB.
+    a.n_pad = (int)(((int64_t)a.b.max_len + kPromptTile - 1) / kPromptTile * kPromptTile);
+    if (a.n_pad == 0) a.n_pad = kPromptTile;
+    const int64_t fit = ((int64_t)1 << 30) / ((int64_t)a.n_pad * d * 4);
+    a.pairs = (int)(fit < 1 ? 1 : fit < all_pairs ? fit : all_pairs);
+  } else if (a.many_rows) {
+    while (a.b.page_tokens % a.box_rows) a.box_rows /= 2;
+  }
   a.cols = a.many_rows ? kPromptCols : kCols;
   a.tile = a.many_rows ? kPromptTile : kKvBlock;
   a.col_tiles = (int)(((int64_t)a.b.max_rows * a.G + a.cols - 1) / a.cols);
@@ -542,7 +559,7 @@ void plan_kv_attention(KvAttnParams &a, int d) {
   int64_t splits;
   if (a.many_rows) {
     // one block an SM, and at least 8 tiles a block
-    splits = 148 / base;
+    splits = 148 / ((int64_t)a.pairs * a.col_tiles);
     if (splits > most / 8) splits = most / 8;
   } else {
     // enough blocks for every SM to hold several, and at least 4 tiles a warp

@@ -30,6 +30,10 @@ struct KvAttnParams {
   int many_rows;  // the tcgen05 kernel
   int cols, tile;
   int col_tiles, tiles_per_split, splits;
+  // many_rows: the (sequence, KV head) pairs of one launch, and the rows of a K
+  // or V box; e4m3: tokens of a pair in the widened copy (0: there is none)
+  int pair0, pairs, box_rows, n_pad;
+  const uint16_t *wide;  // [2][pairs][n_pad][d] bf16
   WsStatus *status;
   int *taint;       // many_rows: [units][splits], see kv_prompt.cu
   float2 *part_ml;  // [splits][num_rows * h_q]: maximum (log2 units), sum
@@ -98,8 +102,8 @@ __device__ __forceinline__ void write_status(const KvAttnParams &a) {
 
 // kv_attention.cu
 cudaError_t launch_kv_attention(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
-void plan_kv_attention(KvAttnParams &a, int d);
-// kv_prompt.cu: the tcgen05 kernel alone
+void plan_kv_attention(KvAttnParams &a, int d, bool f8);
+// kv_prompt.cu: the tcgen05 kernel, and the widening before it
 cudaError_t launch_kv_prompt(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
 
 }  // namespace fathom

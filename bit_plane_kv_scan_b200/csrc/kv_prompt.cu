@@ -16,18 +16,20 @@
 // and 128 keys 4 products of 128 x 128 x 128 take 2048 clocks of the tensor pipe,
 // and 32768 exponentials 2048 clocks of the special-function units.
 //
-// Warps: 0-3 and 4-7 the softmax of the two tiles; 8-11 load Q, K and V into
-// shared memory, by cp.async (bf16) or through registers (e4m3, which becomes
-// bf16 exactly, its power-of-two scale included); 12 issues the MMAs (13-15 are
-// there to give up their registers).  K and V go
-// through a ring of 4 buffers in 128-byte swizzled rows; pages may be as small as
-// 16 tokens.  Keys that no row of the unit sees, and those on bad pages, arrive as
-// zeros.
+// Warps: 0-3 and 4-7 the softmax of the two tiles, 8 loads K and V by TMA (boxes of
+// one page's rows, 128-byte swizzle) into a ring of 4 tiles, 9 issues the MMAs, 10
+// and 11 look after V's edges.  An e4m3 cache is widened first, once for all
+// units: widen_kernel writes the visible keys' bf16 values (exact, the power-of-two
+// scale included) to the workspace, and the units read those.  (Widening inside
+// the units, each for itself, held them to 528 TFLOP/s; loads by cp.async from
+// four warps held bf16 to 807.)
 //
 // Masks are applied to S, where a tile of keys is not seen whole.  A masked key's
-// weight is an exact zero, but 0 * NaN is not: where a value that some row of the
-// unit does not see is not finite, the loading warps mark the unit, and the
-// few-rows kernel (which masks V row by row) does it again afterwards.
+// weight is an exact zero, but 0 * NaN is not.  So in such tiles V's rows that no
+// row of the unit sees become zeros, and where a value that some row does not see
+// is not finite, the unit is marked and the few-rows kernel (which masks V row by
+// row) does it again afterwards.
+#include <cuda.h>
 #include <cuda_fp8.h>
 
 #include "kv_attention.cuh"
@@ -38,15 +40,14 @@ namespace fathom {
 namespace {
 
 constexpr int kSoftWarps = 8;  // 4 for each tile
-constexpr int kLoadWarp0 = kSoftWarps, kLoadWarps = 4;
-constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // 512: the MMA warp's group has no other work
-// Registers: 512 threads are launched with 128 each, 65536 in all.  The softmax
-// keeps a row of 128 scores in registers; the other groups give theirs up:
-// 256 * 192 + 128 * 88 + 128 * 40 = 65536.
-constexpr int kSoftRegs = 192, kLoadRegs = 88, kMmaRegs = 40;
-static_assert(kSoftRegs * 256 + (kLoadRegs + kMmaRegs) * 128 <= 65536, "registers of the block");
-constexpr int kLoadThreads = 32 * kLoadWarps;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kEdgeWarp0 = 10, kEdgeWarps = 2;
+constexpr int kThreads = 32 * (kEdgeWarp0 + kEdgeWarps);  // 384
+constexpr int kEdgeThreads = 32 * kEdgeWarps;
+// Registers: 384 threads are launched with 168 each, 64512 in all.  The softmax
+// keeps a row of 128 scores in registers; the others give theirs up:
+// 256 * 224 + 128 * 56 = 64512.
+constexpr int kSoftRegs = 224, kOtherRegs = 56;
+static_assert(kSoftRegs * 256 + kOtherRegs * 128 <= 168 * kThreads, "registers of the block");
 constexpr int kM = 128;                  // rows of a tile
 constexpr int kN = kPromptTile;          // keys of a tile
 constexpr int kStages = 4;               // ring of K and V tiles
@@ -149,6 +150,24 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// A box of the tensor map from row y and dimension x into shared memory; its bytes
+// count towards the barrier.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}\n" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+
 // Whether one of two bf16 values is an infinity or a NaN.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
@@ -183,38 +202,41 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-// The loading warps' part: pages of one tile of keys, found by the lanes of
-// each warp (lane b: the tile's 16-token block b).
-struct TilePages {
-  int page, slot, key0;
-  bool whole;  // every row of the unit sees every key
+// The units' order of work: later rows see more keys, so they come first.
+struct Unit {
+  int split, pair, rb;
 };
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) {
+__device__ __forceinline__ Unit unit_of(const KvAttnParams &a, int x) {
+  Unit u;
+  u.split = x % a.splits;
+  x /= a.splits;
+  u.pair = a.pair0 + x % a.pairs;
+  u.rb = a.col_tiles - 1 - x / a.pairs;
+  return u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_prompt_kernel(const __grid_constant__ KvAttnParams a, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v) {
   constexpr int kTile = tile_bytes<D>();
   constexpr int kSteps = D / 16;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 1 + 4 + 1];
+  __shared__ __align__(8) uint64_t s_bar[3 * kStages + 2 + 4 + 1];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fault;
-  if (blockIdx.x == gridDim.x - 1) {
-    grid_dependency_wait();
-    allow_dependent_launch();
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if ((int)blockIdx.x == a.pairs * a.col_tiles * a.splits) {  // one more, in the first launch
     write_status(a);
     return;
   }
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // later rows see more keys: their units come first
-  int x = blockIdx.x;
-  const int split = x % a.splits;
-  x /= a.splits;
-  const int hs = x % (a.b.h_kv * a.b.num_seqs);
-  const int rb = a.col_tiles - 1 - x / (a.b.h_kv * a.b.num_seqs);
-  const int head = hs % a.b.h_kv, s = hs / a.b.h_kv;
-  int *taint = a.taint + ((int64_t)(s * a.b.h_kv + head) * a.col_tiles + rb) * a.splits + split;
+  const Unit u = unit_of(a, blockIdx.x);
+  const int split = u.split, rb = u.rb;
+  const int head = u.pair % a.b.h_kv, s = u.pair / a.b.h_kv;
+  int *taint = a.taint + ((int64_t)u.pair * a.col_tiles + rb) * a.splits + split;
   if (tid == 0) *taint = 0;
   const KvSeq q = kv_seq(a.b, s);
   const int c0 = rb * kPromptCols, c1 = min(c0 + kPromptCols, q.rows * a.G);
@@ -230,12 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
   const uint32_t base = (tc_smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sq = base, ring = base + 2 * kTile;
   const uint32_t bar0 = tc_smem_u32(s_bar);
-  auto kv_full = [&](int i) { return bar0 + 8 * i; };
-  auto kv_empty = [&](int i) { return bar0 + 8 * (kStages + i); };
-  const uint32_t q_full = bar0 + 8 * (2 * kStages);
-  auto s_full = [&](int i) { return bar0 + 8 * (2 * kStages + 1 + i); };
-  auto p_full = [&](int i) { return bar0 + 8 * (2 * kStages + 3 + i); };
-  const uint32_t o_full = bar0 + 8 * (2 * kStages + 5);
+  auto kv_full = [&](int i) { return bar0 + 8 * i; };                  // TMA's bytes are there
+  auto kv_empty = [&](int i) { return bar0 + 8 * (kStages + i); };     // the MMAs are done with it
+  auto v_ready = [&](int i) { return bar0 + 8 * (2 * kStages + i); };  // V's edges are in order
+  auto q_full = [&](int i) { return bar0 + 8 * (3 * kStages + i); };
+  auto s_full = [&](int i) { return bar0 + 8 * (3 * kStages + 2 + i); };
+  auto p_full = [&](int i) { return bar0 + 8 * (3 * kStages + 4 + i); };
+  const uint32_t o_full = bar0 + 8 * (3 * kStages + 6);
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
@@ -246,11 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
   }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(kv_full(i), kLoadThreads);
+      mbar_init(kv_full(i), 1);
       mbar_init(kv_empty(i), 1);
+      mbar_init(v_ready(i), kEdgeThreads);
     }
-    mbar_init(q_full, kLoadThreads);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full(i), kM);
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), kM);
     }
@@ -265,7 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
   // tensor memory: S_0, S_1 (P_i over their first half), O_0, O_1
   auto t_s = [&](int i) { return tmem + kN * i; };
   auto t_o = [&](int i) { return tmem + 2 * kN + D * i; };
+  // the page of the token `key`, -1 where there is none
+  auto page_of = [&](int key) {
+    return key < q.len ? kv_page(a.b, s, (int)((unsigned)key / (unsigned)a.b.page_tokens)) : -1;
+  };
+  // whether some row of the unit sees the key
+  auto seen_by_some = [&](int key) {
+    return key <= p_hi && (key > p_lo - a.window || key < a.sinks);
+  };
 
+  // (nt = 0: no row sees anything; the softmax warps write zeros)
   if (warp < kSoftWarps) {
     // ----------------------------------------------------------- softmax --
     regs_up<kSoftRegs>();
@@ -277,14 +310,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
     float ref = -INFINITY, l = 0.0f;
     bool live = true;
     if (nt > 0 && m < n_m) {
+      {  // this thread's row of Q (zeros behind the last); its sign makes cs >= 0
+        const uint32_t flip = a.qscale < 0.0f ? 0x80008000u : 0u;
+        const uint16_t *src = static_cast<const uint16_t *>(a.q) +
+                              (int64_t)(q.row0 + c / a.G) * a.q_stride +
+                              (int64_t)(head * a.G + c % a.G) * D;
+        const bool wide = ((uintptr_t)a.q & 15) == 0 && a.q_stride % 8 == 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (c < c1) {
+            const uint16_t *e = src + 8 * i;
+            if (wide) {
+              x = *reinterpret_cast<const uint4 *>(e);
+            } else {
+              x.x = e[0] | ((uint32_t)e[1] << 16);
+              x.y = e[2] | ((uint32_t)e[3] << 16);
+              x.z = e[4] | ((uint32_t)e[5] << 16);
+              x.w = e[6] | ((uint32_t)e[7] << 16);
+            }
+            x.x ^= flip;
+            x.y ^= flip;
+            x.z ^= flip;
+            x.w ^= flip;
+          }
+          st_shared16(sq + m * kTile + (i / 8) * kPanel + r * 128 + (((i % 8) ^ (r & 7)) << 4), x);
+        }
+        proxy_fence();
+        mbar_arrive(q_full(m));
+      }
       const int t_lo = first + (c0 + m * kM) / a.G;
       const int t_hi = first + (min(c0 + m * kM + kM, c1) - 1) / a.G;
       // blocks of 16 keys that are there, of tile j
       auto blocks_of = [&](int j) {
         const int key = kN * tiles.at(i0 + j) + kKvBlock * (lane & 7);
-        const bool ok = key < q.len &&
-                        kv_page(a.b, s, (int)((unsigned)key / (unsigned)a.b.page_tokens)) >= 0;
-        return __ballot_sync(0xffffffffu, ok) & 0xffu;
+        return __ballot_sync(0xffffffffu, page_of(key) >= 0) & 0xffu;
       };
       uint32_t blocks = blocks_of(0);
       for (int j = 0; j < nt; ++j) {
@@ -420,234 +480,143 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
         }
       }
     }
-  } else if (warp < kMmaWarp) {
-    // ------------------------------------------------------------- loads --
-    // (nt = 0: no row sees anything; the softmax warps write zeros)
-    regs_down<kLoadRegs>();
-    if (nt > 0) {
-    const int t = tid - 32 * kLoadWarp0;
-    {  // Q: rows c0 .. c1 - 1, the rest zeros; its sign makes c >= 0
-      constexpr int kChunks = D / 8;  // 16-byte pieces of a row
-      const uint32_t flip = a.qscale < 0.0f ? 0x80008000u : 0u;
-      const uint16_t *qp = static_cast<const uint16_t *>(a.q);
-      const bool wide = ((uintptr_t)qp & 15) == 0 && a.q_stride % 8 == 0;
-      for (int i = t; i < n_m * kM * kChunks; i += kLoadThreads) {
-        const int r = i / kChunks, ch = i % kChunks, c = c0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < c1) {
-          const uint16_t *src = qp + (int64_t)(q.row0 + c / a.G) * a.q_stride +
-                                (int64_t)(head * a.G + c % a.G) * D + ch * 8;
-          if (wide) {
-            v = *reinterpret_cast<const uint4 *>(src);
-          } else {
-            v.x = src[0] | ((uint32_t)src[1] << 16);
-            v.y = src[2] | ((uint32_t)src[3] << 16);
-            v.z = src[4] | ((uint32_t)src[5] << 16);
-            v.w = src[6] | ((uint32_t)src[7] << 16);
-          }
-          v.x ^= flip;
-          v.y ^= flip;
-          v.z ^= flip;
-          v.w ^= flip;
-        }
-        const int m = r / kM, rr = r % kM;
-        st_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 + (((ch % 8) ^ (rr & 7)) << 4), v);
-      }
-      proxy_fence();
-      mbar_arrive(q_full);
-    }
-    constexpr int kRow = F8 ? D : 2 * D;            // bytes of a row in the cache
-    constexpr int kPer = kRow / 16;                 // 16-byte pieces of a row
-    constexpr int kRows = kLoadThreads / kPer;      // rows that the warps load at once
-    constexpr int kIter = kN / kRows;               // pieces a thread loads of a tile
-    const int piece = t % kPer, r0 = t / kPer;      // this thread's piece of rows r0 + kRows i
-    auto pages_of = [&](int j) {
-      TilePages p;
-      p.key0 = kN * tiles.at(i0 + j);
-      const int key = p.key0 + kKvBlock * (lane & 7);
-      const int at = (int)((unsigned)key / (unsigned)a.b.page_tokens);
-      p.page = key < q.len ? kv_page(a.b, s, at) : -1;
-      p.slot = key - at * a.b.page_tokens;
-      p.whole = sees_all(a, p_lo, p_hi, p.key0, kN);
-      return p;
-    };
-    // the place of row r0 + kRows i of a tile; NULL where there is nothing, or
-    // nothing that a row of the unit sees
-    auto row_of = [&](const TilePages &p, const void *cache, int i) -> const uint8_t * {
-      const int r = r0 + kRows * i;
-      const int page = __shfl_sync(0xffffffffu, p.page, r / kKvBlock);
-      const int slot = __shfl_sync(0xffffffffu, p.slot, r / kKvBlock);
-      const int key = p.key0 + r;
-      if (page < 0 || key > p_hi || (key <= p_lo - a.window && key >= a.sinks)) return nullptr;
-      return static_cast<const uint8_t *>(cache) +
-             (((int64_t)page * a.b.h_kv + head) * a.b.page_tokens + slot + r % kKvBlock) * kRow +
-             piece * 16;
-    };
-    bool live = true;
-    // waits until the ring's buffer of item x is free (every second item is a V)
-    auto claim = [&](int x) {
-      if (x >= kStages && !warp_wait(kv_empty(x % kStages), (x / kStages - 1) & 1)) {
-        live = false;
-        s_fault = 1;
-      }
-      return live;
-    };
-    if constexpr (!F8) {
-      // this thread's piece of row r0 + kRows i sits kRows * 128 bytes after the
-      // one before (kRows is a multiple of 8, so the swizzle is the same)
-      static_assert(kRows % 8 == 0, "a thread's rows share a swizzle phase");
-      const uint32_t my = (piece / 8) * kPanel + r0 * 128 + (((piece % 8) ^ (r0 & 7)) << 4);
-      bool pending_check = false;
-      // an item whose copies have landed is checked (V) and handed over
-      auto finish = [&](int x, bool check) {
-        proxy_fence();
-        if (check) {
-          uint32_t bad = 0;
-#pragma unroll
-          for (int i = 0; i < kIter; ++i) {
-            const uint4 v = ld_shared16(ring + (x % kStages) * kTile + my + i * kRows * 128);
-            bad |= nonfinite2(v.x) | nonfinite2(v.y) | nonfinite2(v.z) | nonfinite2(v.w);
-          }
-          if (bad) *taint = 1;
-        }
-        mbar_arrive(kv_full(x % kStages));
+  } else {
+    regs_down<kOtherRegs>();
+    if (warp == kTmaWarp && nt > 0) {
+      // ----------------------------------------------------------- loads --
+      // a lane per box: box_rows rows of one page, 64 dimensions
+      constexpr int kPanels = D / 64;
+      const int boxes = kN / a.box_rows * kPanels;
+      const int row = lane / kPanels * a.box_rows, panel = lane % kPanels;
+      const bool widened = a.n_pad > 0;
+      const uint32_t bytes = (uint32_t)a.box_rows * 128;
+      const uint32_t to = ring + panel * kPanel + row * 128;
+      // the box's row in the tensor map; -1 where nothing is to be fetched
+      auto place = [&](int j) {
+        const int key = kN * tiles.at(i0 + j) + row, last = key + a.box_rows - 1;
+        if (lane >= boxes || key > p_hi || (last <= p_lo - a.window && key >= a.sinks)) return -1;
+        if (widened) return (u.pair - a.pair0) * a.n_pad + key;
+        const int page = page_of(key);
+        if (page < 0) return -1;
+        return (page * a.b.h_kv + head) * a.b.page_tokens + key % a.b.page_tokens;
       };
-      TilePages p = pages_of(0);
+      bool live = true;
+      int y = place(0);
       for (int j = 0; j < nt && live; ++j) {
-        const TilePages cur = p;
-        if (j + 1 < nt) p = pages_of(j + 1);
+        const int at = y;
+        if (j + 1 < nt) y = place(j + 1);
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, at >= 0));
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-          const int x = 2 * j + side;
-          if (!claim(x)) break;
-          const uint32_t dst = ring + (x % kStages) * kTile + my;
-#pragma unroll
-          for (int i = 0; i < kIter; ++i) {
-            const uint8_t *src = row_of(cur, side ? a.cv : a.ck, i);
-            tc_cp_async16(dst + i * kRows * 128, src ? src : static_cast<const uint8_t *>(a.ck),
-                          src ? 16u : 0u);
+          const int x = 2 * j + side, st = x % kStages;
+          if (x >= kStages && !warp_wait(kv_empty(st), (x / kStages - 1) & 1)) {
+            live = false;
+            s_fault = 1;
+            break;
           }
-          tc_cp_async_commit();
-          if (x > 0) {
-            tc_cp_async_wait<1>();
-            finish(x - 1, pending_check);
-          }
-          pending_check = side && !cur.whole;
+          if (lane == 0) mbar_expect(kv_full(st), n * bytes);
+          __syncwarp();
+          if (at >= 0) tma_box(to + st * kTile, side ? &map_v : &map_k, 64 * panel, at, kv_full(st));
         }
       }
-      tc_cp_async_wait<0>();
-      if (live) finish(2 * nt - 1, pending_check);
-    } else {
-      // the piece's 16 codes become 32 bytes: dimensions 16 piece .. 16 piece + 15
-      static_assert(kRows % 8 == 0 && (kRows <= kKvBlock || kRows % kKvBlock == 0), "");
-      const uint32_t my = (piece / 4) * kPanel + r0 * 128;
-      const uint32_t o0 = ((piece % 4 * 2) ^ (r0 & 7)) << 4, o1 = ((piece % 4 * 2 + 1) ^ (r0 & 7)) << 4;
-      uint4 w[kIter], next[kIter];
-      uint32_t exps = 0, exps_next = 0;
-      auto fetch = [&](const TilePages &p, int side, uint4 (&v)[kIter], uint32_t &ex) {
-        const uint8_t *sc = side ? a.v_scale : a.k_scale;
-        ex = p.page < 0 ? 127u
-                        : (uint32_t)(kv_scale_exp(__ldg(sc + ((int64_t)p.page * a.b.h_kv + head) *
-                                                                (a.b.page_tokens / kKvBlock) +
-                                                        p.slot / kKvBlock)) + 127);
+      // no copy may be on its way when the block ends: the last ones are waited for
+      // by their readers, or here when those have given up
+      if (!live)
+        for (int i = 0; i < kStages; ++i) mbar_wait(kv_full(i), 0);
+    } else if (warp >= kEdgeWarp0 && nt > 0) {
+      // ------------------------------------------------------- V's edges --
+      const int t = tid - 32 * kEdgeWarp0;
+      for (int j = 0; j < nt; ++j) {
+        const int x = 2 * j + 1, st = x % kStages;
+        const int key0 = kN * tiles.at(i0 + j);
+        // a tile that every row sees whole needs nothing, if its pages are there
+        const bool gone = page_of(key0 + kKvBlock * (lane & 7)) < 0;
+        const bool edge =
+            __any_sync(0xffffffffu, gone) || !sees_all(a, p_lo, p_hi, key0, kN);
+        if (!warp_wait(kv_full(st), (x / kStages) & 1)) {
+          s_fault = 1;
+          break;
+        }
+        if (edge) {
+          uint32_t bad = 0;
+          for (int r = t; r < kN; r += kEdgeThreads) {
+            const uint32_t at = ring + st * kTile + r * 128;
+            const bool seen = seen_by_some(key0 + r) && page_of(key0 + r) >= 0;
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const uint8_t *src = row_of(p, side ? a.cv : a.ck, i);
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (src) v[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+            for (int i = 0; i < D / 8; ++i) {
+              const uint32_t w = at + (i / 8) * kPanel + 16 * (i % 8);
+              if (!seen) {
+                st_shared16(w, make_uint4(0, 0, 0, 0));
+              } else {
+                const uint4 v = ld_shared16(w);
+                bad |= nonfinite2(v.x) | nonfinite2(v.y) | nonfinite2(v.z) | nonfinite2(v.w);
+              }
+            }
+          }
+          if (bad) *taint = 1;
+          proxy_fence();
+        }
+        mbar_arrive(v_ready(st));
+      }
+    } else if (warp == kMmaWarp && nt > 0) {
+      // ------------------------------------------------------------ MMAs --
+      constexpr uint32_t kIdS = idesc(kN, false), kIdO = idesc(D, true);
+      const bool leader = tc_elect_one();
+      bool live = mbar_wait(q_full(0), 0);
+      if (n_m == 2 && live) live = mbar_wait(q_full(1), 0);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (live) live = mbar_wait(bar, parity);
+        return live;
+      };
+      auto mul_s = [&](int m, int stage) {
+        if (!leader) return;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
+          mma_ss(t_s(m), smem_desc(sq + m * kTile + off, 16), smem_desc(ring + stage * kTile + off, 16),
+                 kIdS, k > 0);
         }
       };
-      TilePages cur = pages_of(0), p = cur;
-      fetch(cur, 0, w, exps);
-      for (int x = 0; x < 2 * nt && live; ++x) {
-        const int side = x & 1;
-        if (!side && x + 2 < 2 * nt) p = pages_of(x / 2 + 1);
-        // the next item's loads are on their way while this one is widened
-        if (x + 1 < 2 * nt) fetch(side ? p : cur, side ^ 1, next, exps_next);
-        if (!claim(x)) break;
-        const uint32_t dst = ring + (x % kStages) * kTile + my;
-        uint32_t bad = 0;
+      auto mul_o = [&](int m, int stage, bool acc) {
+        if (!leader) return;
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const uint32_t ex = __shfl_sync(0xffffffffu, exps, (r0 + kRows * i) / kKvBlock);
-          const float f = __int_as_float((int)ex << 23);
-          const uint4 v = w[i];
-          const uint2 b0 = widen4(v.x, f), b1 = widen4(v.y, f), b2 = widen4(v.z, f),
-                      b3 = widen4(v.w, f);
-          st_shared16(dst + i * kRows * 128 + o0, make_uint4(b0.x, b0.y, b1.x, b1.y));
-          st_shared16(dst + i * kRows * 128 + o1, make_uint4(b2.x, b2.y, b3.x, b3.y));
-          bad |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
-                 ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
-        }
-        if (side && !cur.whole && (bad & 0x80808080u)) *taint = 1;
-        proxy_fence();
-        mbar_arrive(kv_full(x % kStages));
-        if (side) cur = p;
-        exps = exps_next;
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) w[i] = next[i];
-      }
-    }
-    }
-  } else {
-    // -------------------------------------------------------------- MMAs --
-    regs_down<kMmaRegs>();
-    if (warp == kMmaWarp && nt > 0) {
-    constexpr uint32_t kIdS = idesc(kN, false), kIdO = idesc(D, true);
-    const bool leader = tc_elect_one();
-    bool live = mbar_wait(q_full, 0);
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (live) live = mbar_wait(bar, parity);
-      return live;
-    };
-    auto mul_s = [&](int m, int stage) {
-      if (!leader) return;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
-        mma_ss(t_s(m), smem_desc(sq + m * kTile + off, 16), smem_desc(ring + stage * kTile + off, 16),
-               kIdS, k > 0);
-      }
-    };
-    auto mul_o = [&](int m, int stage, bool acc) {
-      if (!leader) return;
-#pragma unroll
-      for (int k = 0; k < kN / 16; ++k)
-        mma_ts(t_o(m), t_s(m) + 8 * k, smem_desc(ring + stage * kTile + k * 2048, kPanel), kIdO,
-               acc || k > 0);
-    };
-    auto commit = [&](uint32_t bar) {
-      if (leader) tc_commit(bar);
-    };
-    if (wait(kv_full(0), 0)) {
-      tc_fence_after();
-      for (int m = 0; m < n_m; ++m) {
-        mul_s(m, 0);
-        commit(s_full(m));
-      }
-      commit(kv_empty(0));
-    }
-    for (int j = 0; j < nt && live; ++j) {
-      const int xv = 2 * j + 1, xk = 2 * j + 2;  // ring items: V of this tile, K of the next
-      const bool more = j + 1 < nt;
-      if (!wait(kv_full(xv % kStages), (xv / kStages) & 1)) break;
-      if (more && !wait(kv_full(xk % kStages), (xk / kStages) & 1)) break;
-      for (int m = 0; m < n_m; ++m) {
-        if (!wait(p_full(m), j & 1)) break;
+        for (int k = 0; k < kN / 16; ++k)
+          mma_ts(t_o(m), t_s(m) + 8 * k, smem_desc(ring + stage * kTile + k * 2048, kPanel), kIdO,
+                 acc || k > 0);
+      };
+      auto commit = [&](uint32_t bar) {
+        if (leader) tc_commit(bar);
+      };
+      if (wait(kv_full(0), 0)) {
         tc_fence_after();
-        mul_o(m, xv % kStages, j > 0);
-        if (m == n_m - 1) commit(kv_empty(xv % kStages));
-        if (more) {
-          mul_s(m, xk % kStages);
+        for (int m = 0; m < n_m; ++m) {
+          mul_s(m, 0);
           commit(s_full(m));
         }
+        commit(kv_empty(0));
       }
-      if (more) commit(kv_empty(xk % kStages));
-    }
-    commit(o_full);
-    if (!live) s_fault = 1;
+      for (int j = 0; j < nt && live; ++j) {
+        const int xv = 2 * j + 1, xk = 2 * j + 2;  // ring items: V of this tile, K of the next
+        const bool more = j + 1 < nt;
+        if (!wait(v_ready(xv % kStages), (j >> 1) & 1)) break;
+        if (more && !wait(kv_full(xk % kStages), (xk / kStages) & 1)) break;
+        for (int m = 0; m < n_m; ++m) {
+          if (!wait(p_full(m), j & 1)) break;
+          tc_fence_after();
+          mul_o(m, xv % kStages, j > 0);
+          if (m == n_m - 1) commit(kv_empty(xv % kStages));
+          if (more) {
+            mul_s(m, xk % kStages);
+            commit(s_full(m));
+          }
+        }
+        if (more) commit(kv_empty(xk % kStages));
+      }
+      commit(o_full);
+      if (!live) s_fault = 1;
     }
   }
+
   // Every MMA is complete once o_full has arrived; then the ring's last commits
   // are waited for, so that no arrival is pending when the barriers go away.
   tc_fence_before();
@@ -668,21 +637,108 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvAttnParams a) 
                  : "memory");
 }
 
-template <int D, bool F8>
-cudaError_t launch(const KvAttnParams &a, cudaStream_t s) {
+// E4M3: the keys that some row sees, K and V, as bf16 in [pair - pair0][n_pad][D].  A
+// block per 128 keys of a pair; bound by bytes (1 read, 2 written an element).
+constexpr int kWidenThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_constant__ KvAttnParams a,
+                                                              uint16_t *wide_k, uint16_t *wide_v) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  constexpr int kPieces = D / 16;
+  const int per = a.n_pad / kN;
+  const int pair = blockIdx.x / per, key0 = blockIdx.x % per * kN;
+  const int head = (a.pair0 + pair) % a.b.h_kv, s = (a.pair0 + pair) / a.b.h_kv;
+  const KvSeq q = kv_seq(a.b, s);
+  if (q.rows == 0 || key0 >= q.len) return;
+  const int from = q.len - q.rows - a.window;  // the last key before every row's window
+  if (key0 + kN - 1 <= from && key0 >= a.sinks) return;
+  for (int i = threadIdx.x; i < kN * kPieces; i += kWidenThreads) {
+    const int r = i / kPieces, piece = i % kPieces, key = key0 + r;
+    if (key >= q.len) return;
+    const int at = (int)((unsigned)key / (unsigned)a.b.page_tokens);
+    const int page = kv_page(a.b, s, at);
+    if (page < 0) continue;
+    const int slot = key - at * a.b.page_tokens;
+    const int64_t h = (int64_t)page * a.b.h_kv + head;
+    const int64_t src = (h * a.b.page_tokens + slot) * D + piece * 16;
+    const int64_t sc = h * (a.b.page_tokens / kKvBlock) + slot / kKvBlock;
+    const int64_t dst = ((int64_t)pair * a.n_pad + key) * D + piece * 16;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(
+          static_cast<const uint8_t *>(side ? a.cv : a.ck) + src));
+      const float f = exp2i(kv_scale_exp(__ldg((side ? a.v_scale : a.k_scale) + sc)));
+      const uint2 w0 = widen4(v.x, f), w1 = widen4(v.y, f), w2 = widen4(v.z, f), w3 = widen4(v.w, f);
+      uint4 *out = reinterpret_cast<uint4 *>((side ? wide_v : wide_k) + dst);
+      out[0] = make_uint4(w0.x, w0.y, w1.x, w1.y);
+      out[1] = make_uint4(w2.x, w2.y, w3.x, w3.y);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host --
+
+// A [rows][d] bf16 matrix in boxes of box_rows x 64, 128-byte swizzle.
+cudaError_t make_map(CUtensorMap *map, const void *ptr, int64_t rows, int d, int box_rows) {
+  using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = []() -> Encode {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<Encode>(fn);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims,
+                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch(KvAttnParams a, bool f8, cudaStream_t s) {
   constexpr int smem = smem_bytes<D>();
-  const cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D, F8>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles * a.splits + 1;
-  return launch_dependent(kv_prompt_kernel<D, F8>, dim3((unsigned)blocks), dim3(kThreads), smem, s, a);
+  CUtensorMap map_k, map_v;
+  const void *k = f8 ? a.wide : a.ck;
+  const void *v = f8 ? a.wide + (size_t)a.pairs * a.n_pad * D : a.cv;
+  const int64_t rows = f8 ? (int64_t)a.pairs * a.n_pad
+                          : (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
+  e = make_map(&map_k, k, rows, D, a.box_rows);
+  if (e == cudaSuccess) e = make_map(&map_v, v, rows, D, a.box_rows);
+  const int all = a.b.num_seqs * a.b.h_kv, group = a.pairs;
+  for (a.pair0 = 0; a.pair0 < all && e == cudaSuccess; a.pair0 += group) {
+    a.pairs = all - a.pair0 < group ? all - a.pair0 : group;
+    if (f8)
+      e = launch_dependent(widen_kernel<D>, dim3((unsigned)(a.pairs * (a.n_pad / kN))),
+                           dim3(kWidenThreads), 0, s, a, const_cast<uint16_t *>(a.wide),
+                           static_cast<uint16_t *>(const_cast<void *>(v)));
+    if (e == cudaSuccess)
+      e = launch_dependent(kv_prompt_kernel<D>,
+                           dim3((unsigned)(a.pairs * a.col_tiles * a.splits + (a.pair0 == 0))),
+                           dim3(kThreads), smem, s, a, map_k, map_v);
+  }
+  return e;
 }
 
 }  // namespace
 
 cudaError_t launch_kv_prompt(const KvAttnParams &a, int d, bool f8, cudaStream_t s) {
-  if (d == 128) return f8 ? launch<128, true>(a, s) : launch<128, false>(a, s);
-  if (d == 64) return f8 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+  if (d == 128) return launch<128>(a, f8, s);
+  if (d == 64) return launch<64>(a, f8, s);
   return cudaErrorInvalidValue;
 }
 
