@@ -11,18 +11,19 @@
 // dimensions) as the 16 rows and up to 8 (token, head) pairs as the 8 columns.
 // (The tcgen05 MMAs need 64 rows or more of one operand in shared memory and an
 // accumulator in tensor memory; with 8 columns of work their set-up costs more
-// than the product.)  The order of the contracted index is free, so K and V go
-// straight from global memory into the registers that the MMAs read, 16 bytes a
-// lane, without shared memory:
-//   S^T = K q^T: lane (g, t) holds, of keys g and g + 8, the row's pieces t of
+// than the product.)  The order of the contracted index is free, so lanes read K
+// and V from shared memory 16 bytes at a time, just as the rows lie there:
+//   S^T = K q^T: lane (g, t) holds, of keys g and g + 8, the pieces t of
 //     every four; q's fragments are permuted in the same way.
 //   O^T = V^T P^T: lane (g, t) holds, of keys 2t, 2t + 1, 2t + 8, 2t + 9, the
-//     row's pieces g of every eight; byte permutes pair two keys' elements.
+//     pieces g of every eight; byte permutes pair two keys' elements.
 //     P^T comes from S^T by movmatrix.
-// Each warp takes every fourth 16-key tile of its block's run of tiles and loads
-// the next one while it works on the current one.  The four warps' results meet
-// in shared memory; where a sequence's tiles are split over several blocks, a
-// second kernel joins the blocks' results (maximum, sum, output).
+// Each warp takes every fourth 16-key tile of its block's run of tiles, through a
+// ring of its own in shared memory that 16-byte asynchronous copies fill 2 to 5
+// tiles ahead (no barrier between warps); its lanes look up the pages and scales
+// of 32 tiles at once, a batch ahead.  The four warps' results meet in shared
+// memory; where a sequence's tiles are split over several blocks, a second kernel
+// joins the blocks' results (maximum, sum, output).
 //
 // E4M3: codes become fp16 exactly (the hardware's conversion).  q is scaled to
 // fp16 by a power of two per row and head; a 16-key tile is one scale block, so
@@ -38,6 +39,7 @@
 #include <cuda_fp8.h>
 
 #include "kv_attention.cuh"
+#include "tc_common.cuh"
 
 namespace fathom {
 
@@ -96,15 +98,15 @@ __device__ __forceinline__ uint32_t split16(float &a, float &b) {
 }
 
 template <int BYTES>
-__device__ __forceinline__ void load_bytes(const uint8_t *p, uint32_t *w) {
+__device__ __forceinline__ void load_bytes(uint32_t p, uint32_t *w) {
   if constexpr (BYTES == 16) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(p));
+                 : "r"(p));
   } else if constexpr (BYTES == 8) {
-    asm volatile("ld.global.nc.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
   } else {
-    asm volatile("ld.global.nc.b32 %0, [%1];\n" : "=r"(w[0]) : "l"(p));
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(w[0]) : "r"(p));
   }
 }
 
@@ -115,57 +117,34 @@ struct Shape {
   static constexpr int kVVec = (kRow / 8) % 16 == 0 ? 16 : ((kRow / 8) % 8 == 0 ? 8 : 4);
   static constexpr int kKWords = kRow / 16, kVWords = kRow / 32;  // words a lane has of a row
   static constexpr int kElt = F8 ? 1 : 2;
+  // A warp's ring: 16 rows of K, 16 of V, each row 16 bytes longer than it is
+  // (an odd number of 16-byte pieces: the pieces that 8 lanes read at once lie
+  // in different banks).
+  static constexpr int kPitch = kRow + 16, kSide = kKvBlock * kPitch, kStage = 2 * kSide;
+  static constexpr int kDepth = kRow <= 64 ? 6 : kRow <= 128 ? 4 : 3;
+  static constexpr int kSmem = kWarps * kDepth * kStage;
+  // The byte of piece j of the lane's part of a K row: two neighbouring pieces of
+  // 128 bytes, so that four lanes' pieces 0 are every second one.
+  __device__ static constexpr int k_byte(int j, int t) {
+    return kRow % 128 == 0 ? (j >> 1) * 128 + (2 * t + (j & 1)) * 16 : (j * 4 + t) * kKVec;
+  }
+  __device__ static constexpr int v_byte(int j, int g) { return (j * 8 + g) * kVVec; }
   // the dimension of element e of the lane's part of a K or V row
   __device__ static int k_dim(int e, int t) {
     constexpr int v = kKVec / kElt;
-    return (e / v) * 4 * v + t * v + e % v;
+    return k_byte(e / v, t) / kElt + e % v;
   }
   __device__ static int v_dim(int e, int g) {
     constexpr int v = kVVec / kElt;
-    return (e / v) * 8 * v + g * v + e % v;
+    return v_byte(e / v, g) / kElt + e % v;
   }
 };
 
-template <int D, bool F8>
-struct Tile {
-  uint32_t k[2][Shape<D, F8>::kKWords];
-  uint32_t v[4][Shape<D, F8>::kVWords];
-  float k_scale, v_scale;
-  int key0;  // first key; -1: nothing there
+// What the lanes of a warp have found out about 32 tiles, one each.
+struct Found {
+  int page, slot;  // page -1: nothing there
+  int scales;      // E4M3: K's byte, V's byte
 };
-
-template <int D, bool F8>
-__device__ __forceinline__ void load_tile(const KvAttnParams &a, int s, int head, int key0, int lane,
-                                          Tile<D, F8> &x) {
-  using S = Shape<D, F8>;
-  const int g = lane >> 2, t = lane & 3;
-  const int at = (int)((unsigned)key0 / (unsigned)a.b.page_tokens);
-  const int page = kv_page(a.b, s, at);
-  x.key0 = page < 0 ? -1 : key0;
-  if (page < 0) return;
-  const int slot = key0 - at * a.b.page_tokens;
-  const int64_t h = (int64_t)page * a.b.h_kv + head;
-  const int64_t off = (h * a.b.page_tokens + slot) * S::kRow;
-  const uint8_t *kp = static_cast<const uint8_t *>(a.ck) + off;
-  const uint8_t *vp = static_cast<const uint8_t *>(a.cv) + off;
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int j = 0; j < S::kKWords * 4 / S::kKVec; ++j)
-      load_bytes<S::kKVec>(kp + (g + 8 * r) * S::kRow + (j * 4 + t) * S::kKVec,
-                           &x.k[r][j * S::kKVec / 4]);
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int j = 0; j < S::kVWords * 4 / S::kVVec; ++j)
-      load_bytes<S::kVVec>(vp + (2 * t + (r & 1) + 8 * (r >> 1)) * S::kRow + (j * 8 + g) * S::kVVec,
-                           &x.v[r][j * S::kVVec / 4]);
-  if constexpr (F8) {
-    const int64_t b = h * (a.b.page_tokens / kKvBlock) + slot / kKvBlock;
-    x.k_scale = exp2i(kv_scale_exp(__ldg(a.k_scale + b)));
-    x.v_scale = exp2i(kv_scale_exp(__ldg(a.v_scale + b)));
-  }
-}
 
 // O^T += V^T P^T for one 16-key tile; with PART only into this lane's columns
 // that `mine` names.
@@ -212,7 +191,10 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
   constexpr int kSteps = D / 16;
   constexpr float kShift = F8 ? 15.0f : 0.0f;
   __shared__ float s_m[kWarps][kCols], s_l[kWarps][kCols];
-  __shared__ float s_o[kWarps][kCols][D + 4];
+  extern __shared__ __align__(16) unsigned char s_ring[];
+  // the warps' outputs meet where the rings were
+  float(*s_o)[kCols][D + 4] = reinterpret_cast<float(*)[kCols][D + 4]>(s_ring);
+  static_assert(sizeof(float) * kWarps * kCols * (D + 4) <= S::kSmem, "outputs fit in the rings");
   const KvSeq q = kv_seq(a.b, s);
   const int c0 = ct * kCols, c1 = min(c0 + kCols, q.rows * a.G);  // columns of this block
   if (c0 >= c1) return;
@@ -272,33 +254,49 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
 
-  auto fold = [&](const Tile<D, F8> &x) {
-    if (x.key0 < 0) return;
-    float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // the tile of keys key0 .. key0 + 15 in the ring at shared address `at`
+  auto fold = [&](int key0, uint32_t at, float k_scale, float v_scale) {
+    float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sc2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    {
+      uint32_t k[2][S::kKWords];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      uint32_t f[4];
-      if constexpr (F8) {
-        f[0] = e4m3_half2(x.k[0][i]);
-        f[1] = e4m3_half2(x.k[1][i]);
-        f[2] = e4m3_half2(x.k[0][i] >> 16);
-        f[3] = e4m3_half2(x.k[1][i] >> 16);
-      } else {
-        f[0] = x.k[0][2 * i];
-        f[1] = x.k[1][2 * i];
-        f[2] = x.k[0][2 * i + 1];
-        f[3] = x.k[1][2 * i + 1];
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < S::kKWords * 4 / S::kKVec; ++j)
+          load_bytes<S::kKVec>(at + (g + 8 * r) * S::kPitch + S::k_byte(j, t), &k[r][j * S::kKVec / 4]);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        uint32_t f[4];
+        if constexpr (F8) {
+          f[0] = e4m3_half2(k[0][i]);
+          f[1] = e4m3_half2(k[1][i]);
+          f[2] = e4m3_half2(k[0][i] >> 16);
+          f[3] = e4m3_half2(k[1][i] >> 16);
+        } else {
+          f[0] = k[0][2 * i];
+          f[1] = k[1][2 * i];
+          f[2] = k[0][2 * i + 1];
+          f[3] = k[1][2 * i + 1];
+        }
+#pragma unroll
+        for (int u = 0; u < TERMS; ++u)  // two sums, so that half as many wait for each other
+          mma16<F8>(i & 1 ? sc2 : sc, f, qf[u][i][0], qf[u][i][1]);
       }
-#pragma unroll
-      for (int u = 0; u < TERMS; ++u) mma16<F8>(sc, f, qf[u][i][0], qf[u][i][1]);
     }
+    uint32_t xv[4][S::kVWords];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sc[e] *= F8 ? cs[e & 1] * x.k_scale : cs[e & 1];
-    const bool whole = sees_all(a, p_lo, p_hi, x.key0, kKvBlock);
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < S::kVWords * 4 / S::kVVec; ++j)
+        load_bytes<S::kVVec>(at + S::kSide + (2 * t + (r & 1) + 8 * (r >> 1)) * S::kPitch + S::v_byte(j, g),
+                             &xv[r][j * S::kVVec / 4]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[e] = (sc[e] + sc2[e]) * (F8 ? cs[e & 1] * k_scale : cs[e & 1]);
+    const bool whole = sees_all(a, p_lo, p_hi, key0, kKvBlock);
     if (!whole) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (!sees(a, pc[e & 1], x.key0 + g + 8 * (e >> 1))) sc[e] = -INFINITY;
+        if (!sees(a, pc[e & 1], key0 + g + 8 * (e >> 1))) sc[e] = -INFINITY;
     }
     float corr[2];
     float mn[2];
@@ -336,7 +334,7 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
       p1[u] = transpose8(split16<F8>(p[2], p[3]));
     }
     if (whole) {
-      add_pv<D, F8, TERMS, false>(o, x.v, x.v_scale, p0, p1, {true, true});
+      add_pv<D, F8, TERMS, false>(o, xv, v_scale, p0, p1, {true, true});
       return;
     }
     // token by token: V rows that the token does not see become zeros, and only
@@ -346,29 +344,76 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
       const bool mine[2] = {pc[0] == pos, pc[1] == pos};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const bool see = sees(a, pos, x.key0 + 2 * t + (r & 1) + 8 * (r >> 1));
+        const bool see = sees(a, pos, key0 + 2 * t + (r & 1) + 8 * (r >> 1));
 #pragma unroll
-        for (int w = 0; w < S::kVWords; ++w) v[r][w] = see ? x.v[r][w] : 0u;
+        for (int w = 0; w < S::kVWords; ++w) v[r][w] = see ? xv[r][w] : 0u;
       }
-      add_pv<D, F8, TERMS, true>(o, v, x.v_scale, p0, p1, mine);
+      add_pv<D, F8, TERMS, true>(o, v, v_scale, p0, p1, mine);
     }
   };
 
-  auto key_of = [&](int i) { return kKvBlock * tiles.at(i); };
-  // two tiles in flight: the next one's loads are issued before the current one
-  // is worked on
-  Tile<D, F8> ta, tb;
-  int i = i0 + warp;
-  if (i < i1) load_tile<D, F8>(a, s, head, key_of(i), lane, ta);
-  while (i < i1) {
-    if (i + kWarps < i1) load_tile<D, F8>(a, s, head, key_of(i + kWarps), lane, tb);
-    fold(ta);
-    i += kWarps;
-    if (i >= i1) break;
-    if (i + kWarps < i1) load_tile<D, F8>(a, s, head, key_of(i + kWarps), lane, ta);
-    fold(tb);
-    i += kWarps;
+  // this warp's tiles: number n is tile i0 + warp + kWarps n
+  const int mine = i1 - i0 - warp > 0 ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;
+  auto key_of = [&](int n) { return kKvBlock * tiles.at(i0 + warp + kWarps * n); };
+  // lane l looks up tile 32 batch + l: page, place and scales, far ahead of use
+  auto look = [&](int batch) {
+    Found x = {-1, 0, 0};
+    const int n = 32 * batch + lane;
+    if (n < mine) {
+      const int key = key_of(n);
+      const int at = (int)((unsigned)key / (unsigned)a.b.page_tokens);
+      x.page = kv_page(a.b, s, at);
+      x.slot = key - at * a.b.page_tokens;
+      if (F8 && x.page >= 0) {
+        const int64_t i = ((int64_t)x.page * a.b.h_kv + head) * (a.b.page_tokens / kKvBlock) +
+                          x.slot / kKvBlock;
+        x.scales = __ldg(a.k_scale + i) | (__ldg(a.v_scale + i) << 8);
+      }
+    }
+    return x;
+  };
+  Found cur = look(0), next = look(1);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) + warp * S::kDepth * S::kStage;
+  int batch = 0;  // of `cur`
+  // starts the copy of tile n (of batch or batch + 1) into its place in the ring
+  auto issue = [&](int n) {
+    if (n < mine) {
+      const bool here = n >> 5 == batch;
+      const int page = __shfl_sync(0xffffffffu, here ? cur.page : next.page, n & 31);
+      const int slot = __shfl_sync(0xffffffffu, here ? cur.slot : next.slot, n & 31);
+      if (page >= 0) {
+        const int64_t off = (((int64_t)page * a.b.h_kv + head) * a.b.page_tokens + slot) * S::kRow;
+        const uint32_t to = ring + n % S::kDepth * S::kStage;
+#pragma unroll
+        for (int u = 0; u < S::kRow / 32; ++u) {
+          const int i = lane + 32 * u, r = i / (S::kRow / 16), c = i % (S::kRow / 16);
+          const uint32_t dst = to + r * S::kPitch + c * 16;
+          tc_cp_async16(dst, static_cast<const uint8_t *>(a.ck) + off + i * 16, 16);
+          tc_cp_async16(dst + S::kSide, static_cast<const uint8_t *>(a.cv) + off + i * 16, 16);
+        }
+      }
+    }
+    tc_cp_async_commit();
+  };
+#pragma unroll
+  for (int n = 0; n < S::kDepth - 1; ++n) issue(n);
+  for (int n = 0; n < mine; ++n) {
+    if (n >> 5 != batch) {
+      batch = n >> 5;
+      cur = next;
+      next = look(batch + 1);
+    }
+    tc_cp_async_wait<S::kDepth - 2>();  // tile n's own copies have landed,
+    __syncwarp();                       // and the other lanes'; tile n - 1 has been read
+    issue(n + S::kDepth - 1);
+    const int page = __shfl_sync(0xffffffffu, cur.page, n & 31);
+    const int sc = __shfl_sync(0xffffffffu, cur.scales, n & 31);
+    if (page >= 0)
+      fold(key_of(n), ring + n % S::kDepth * S::kStage, exp2i(kv_scale_exp(sc & 255)),
+           exp2i(kv_scale_exp(sc >> 8)));
   }
+  tc_cp_async_wait<0>();
+  __syncthreads();  // the rings are free
 
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -489,26 +534,34 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, in
   if (lane == 0 && a.lse) a.lse[rh] = lse_of(M, L, shift);
 }
 
+template <int D, bool F8, typename Kernel>
+cudaError_t launch_ring(Kernel kernel, int64_t blocks, const KvAttnParams &a, cudaStream_t s) {
+  constexpr int smem = Shape<D, F8>::kSmem;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, s, a);
+}
+
 template <int D, bool F8>
 cudaError_t launch_redo(const KvAttnParams &a, cudaStream_t s) {
   const int units = a.b.num_seqs * a.b.h_kv * a.col_tiles;
-  return launch_dependent(kv_redo_kernel<D, F8>, dim3(units < 444 ? units : 444), dim3(kThreads), 0,
-                          s, a);
+  return launch_ring<D, F8>(kv_redo_kernel<D, F8>, units < 296 ? units : 296, a, s);
 }
 
 template <int D>
 cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
   const int64_t blocks = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles * a.splits + 1;
-  const dim3 grid((unsigned)blocks), block(kThreads);
+  const dim3 block(kThreads);
   cudaError_t e;
   if (a.many_rows)
     e = launch_kv_prompt(a, D, f8, s);
   else if (f8)
-    e = a.q_bf16 ? launch_dependent(kv_attention_kernel<D, true, 1>, grid, block, 0, s, a)
-                 : launch_dependent(kv_attention_kernel<D, true, 2>, grid, block, 0, s, a);
+    e = a.q_bf16 ? launch_ring<D, true>(kv_attention_kernel<D, true, 1>, blocks, a, s)
+                 : launch_ring<D, true>(kv_attention_kernel<D, true, 2>, blocks, a, s);
   else
-    e = a.q_bf16 ? launch_dependent(kv_attention_kernel<D, false, 1>, grid, block, 0, s, a)
-                 : launch_dependent(kv_attention_kernel<D, false, 3>, grid, block, 0, s, a);
+    e = a.q_bf16 ? launch_ring<D, false>(kv_attention_kernel<D, false, 1>, blocks, a, s)
+                 : launch_ring<D, false>(kv_attention_kernel<D, false, 3>, blocks, a, s);
   if (e == cudaSuccess && a.splits > 1) {
     const int64_t rh = (int64_t)a.b.num_rows * a.h_q;
     e = launch_dependent(kv_combine_kernel, dim3((unsigned)((rh + kWarps - 1) / kWarps)), block, 0,
