@@ -72,11 +72,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
-// Two e4m3 codes to two fp16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3_half2(uint32_t two) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(d) : "h"((uint16_t)two));
-  return d;
+// Four e4m3 codes to four fp16 values, exactly.
+__device__ __forceinline__ void e4m3_half4(uint32_t four, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+
+// 2^x, results below 2^-126 to 0 (hardware; off by 2^-22 of the value).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Two floats as 16-bit terms (a in the low half); what is left goes back.
@@ -159,10 +169,8 @@ __device__ __forceinline__ void add_pv(float (&o)[D / 16][4], const uint32_t (&v
       const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
       const uint32_t lo = __byte_perm(v[0][i / 2], v[1][i / 2], sel);
       const uint32_t hi = __byte_perm(v[2][i / 2], v[3][i / 2], sel);
-      f[0] = e4m3_half2(lo);
-      f[1] = e4m3_half2(lo >> 16);
-      f[2] = e4m3_half2(hi);
-      f[3] = e4m3_half2(hi >> 16);
+      e4m3_half4(lo, f[0], f[1]);
+      e4m3_half4(hi, f[2], f[3]);
     } else {
       f[0] = __byte_perm(v[0][i], v[1][i], 0x5410);
       f[1] = __byte_perm(v[0][i], v[1][i], 0x7632);
@@ -268,10 +276,8 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
       for (int i = 0; i < kSteps; ++i) {
         uint32_t f[4];
         if constexpr (F8) {
-          f[0] = e4m3_half2(k[0][i]);
-          f[1] = e4m3_half2(k[1][i]);
-          f[2] = e4m3_half2(k[0][i] >> 16);
-          f[3] = e4m3_half2(k[1][i] >> 16);
+          e4m3_half4(k[0][i], f[0], f[2]);
+          e4m3_half4(k[1][i], f[1], f[3]);
         } else {
           f[0] = k[0][2 * i];
           f[1] = k[1][2 * i];
@@ -311,7 +317,7 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
     if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        corr[j] = mn[j] == -INFINITY ? 1.0f : exp2f(m[j] - mn[j]);
+        corr[j] = mn[j] == -INFINITY ? 1.0f : ex2(m[j] - mn[j]);
         l[j] *= corr[j];
         m[j] = mn[j];
       }
@@ -324,7 +330,7 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float ref = m[e & 1] == -INFINITY ? 0.0f : m[e & 1] - kShift;
-      p[e] = exp2f(sc[e] - ref);
+      p[e] = ex2(sc[e] - ref);
       l[e & 1] += p[e];
     }
     uint32_t p0[TERMS], p1[TERMS];
@@ -495,13 +501,17 @@ __global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
   }
 }
 
-// Joins the splits of one (row, head): a warp each.
-__global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, int d, float shift) {
+// Joins the splits of one (row, head): a block each, its warps every fourth split.
+// The splits' maxima and sums are read 32 at a time, their outputs 8 at a time, so
+// that their latency is not paid split by split.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, float shift) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t rh = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (rh >= (int64_t)a.b.num_rows * a.h_q) return;
+  constexpr int kPer = D / 32;
+  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t rh = blockIdx.x;
   const int row = (int)(rh / a.h_q), h = (int)(rh % a.h_q);
   const int s = a.b.q_start ? find_seq(a.b.num_seqs, row, [&](int i) { return a.b.q_start[i]; }) : row;
   const KvSeq q = kv_seq(a.b, s);
@@ -511,27 +521,65 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, in
   const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
   const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
   const int64_t step = (int64_t)a.b.num_rows * a.h_q;
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[i * step + rh].x);
+  const int mine = n > warp ? (n - warp + kWarps - 1) / kWarps : 0;
+  float m = -INFINITY, l = 0.0f, o[kPer];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float L = 0.0f, o[FATHOM_MAX_D / 32];
+  for (int j = 0; j < kPer; ++j) o[j] = 0.0f;
+  for (int i0 = 0; i0 < mine; i0 += 32) {
+    const int split = warp + kWarps * (i0 + lane);
+    const float2 ml = split < n ? a.part_ml[split * step + rh] : make_float2(-INFINITY, 0.0f);
+    float big = ml.x;
 #pragma unroll
-  for (int j = 0; j < FATHOM_MAX_D / 32; ++j) o[j] = 0.0f;
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = a.part_ml[i * step + rh];
-    const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
-    L = fmaf(ml.y, f, L);
-    const float *po = a.part_o + (i * step + rh) * d;
+    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    const float next = fmaxf(m, big);
+    const float corr = next == -INFINITY ? 1.0f : exp2f(m - next);
+    // (a split that saw nothing has -inf, 0 and zeros; NaN stays NaN)
+    const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : exp2f(ml.x - next);
+    float sum = ml.y * f;
 #pragma unroll
-    for (int j = 0; j < FATHOM_MAX_D / 32; ++j)
-      if (32 * j < d) o[j] = fmaf(po[32 * j + lane], f, o[j]);
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    l = l * corr + sum;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) o[j] *= corr;
+    m = next;
+    const int here = min(32, mine - i0);
+    for (int k0 = 0; k0 < here; k0 += 8) {
+      float v[8][kPer];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float *po = a.part_o + ((warp + kWarps * (int64_t)(i0 + k0 + k)) * step + rh) * D + lane;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[k][j] = k0 + k < here ? po[32 * j] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (k0 + k < here) o[j] = fmaf(v[k][j], w, o[j]);
+      }
+    }
+  }
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
   }
 #pragma unroll
-  for (int j = 0; j < FATHOM_MAX_D / 32; ++j)
-    if (32 * j < d)
-      store_out(a, rh * d + 32 * j + lane, L > 0.0f ? o[j] / L : (L == 0.0f ? 0.0f : L));
-  if (lane == 0 && a.lse) a.lse[rh] = lse_of(M, L, shift);
+  for (int j = 0; j < kPer; ++j) s_o[warp][32 * j + lane] = o[j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < D; c += kThreads) {
+    float M = -INFINITY, L = 0.0f, O = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = s_m[w] == -INFINITY ? (s_l[w] == 0.0f ? 0.0f : s_l[w]) : exp2f(s_m[w] - M);
+      L = fmaf(s_l[w], f, L);
+      O = fmaf(s_o[w][c], f, O);
+    }
+    store_out(a, rh * D + c, L > 0.0f ? O / L : (L == 0.0f ? 0.0f : L));
+    if (c == 0 && a.lse) a.lse[rh] = lse_of(M, L, shift);
+  }
 }
 
 template <int D, bool F8, typename Kernel>
@@ -564,8 +612,8 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
                  : launch_ring<D, false>(kv_attention_kernel<D, false, 3>, blocks, a, s);
   if (e == cudaSuccess && a.splits > 1) {
     const int64_t rh = (int64_t)a.b.num_rows * a.h_q;
-    e = launch_dependent(kv_combine_kernel, dim3((unsigned)((rh + kWarps - 1) / kWarps)), block, 0,
-                         s, a, D, f8 && !a.many_rows ? 15.0f : 0.0f);
+    e = launch_dependent(kv_combine_kernel<D>, dim3((unsigned)rh), block, 0, s, a,
+                         f8 && !a.many_rows ? 15.0f : 0.0f);
   }
   if constexpr (D == 64 || D == 128)
     if (e == cudaSuccess && a.many_rows)
@@ -574,6 +622,15 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
 }
 
 }  // namespace
+
+// Blocks of the few-rows kernel that the device holds at once, by shared memory
+// (228 KB an SM, 1 KB of it for each block).
+static int kv_resident_blocks(int d, bool f8) {
+  const int row = f8 ? d : 2 * d, depth = row <= 64 ? 6 : row <= 128 ? 4 : 3;
+  const int smem = kWarps * depth * 2 * kKvBlock * (row + 16) + 1280;
+  const int per = 228 * 1024 / smem;
+  return 148 * (per > 4 ? 4 : per);
+}
 
 void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
   // The tcgen05 kernel multiplies 256 columns at a time: it takes over where
@@ -615,8 +672,8 @@ void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
     splits = 148 / ((int64_t)a.pairs * a.col_tiles);
     if (splits > most / 8) splits = most / 8;
   } else {
-    // enough blocks for every SM to hold several, and at least 4 tiles a warp
-    const int64_t want = (8 * 148 + base - 1) / base;
+    // as many blocks as the SMs hold at once, and at least 4 tiles a warp
+    const int64_t want = kv_resident_blocks(d, f8) / base > 0 ? kv_resident_blocks(d, f8) / base : 1;
     splits = most / (4 * kWarps);
     if (splits > want) splits = want;
   }
