@@ -169,9 +169,15 @@ fathom_status check_scan_common(int64_t n, int d, int h_q, int h_kv, int k, int 
 }
 
 // ---------------------------------------------------------- paged KV cache --
-// The current device: the calls on a paged cache check that every pointer
-// belongs to it, since their launches go there.
-fathom_status check_on_device(const void *p, const char *name, size_t align) {
+int current_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+  return dev;
+}
+
+// The calls on a paged cache check that every pointer belongs to the current
+// device `dev`, where their launches go.
+fathom_status check_on_device(const void *p, const char *name, size_t align, int dev) {
   if (p == nullptr) return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s is NULL", name);
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
@@ -180,8 +186,7 @@ fathom_status check_on_device(const void *p, const char *name, size_t align) {
   }
   if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
     return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s is not a device pointer", name);
-  int dev = 0;
-  if (a.type == cudaMemoryTypeDevice && cudaGetDevice(&dev) == cudaSuccess && a.device != dev)
+  if (a.type == cudaMemoryTypeDevice && a.device != dev)
     return fail(FATHOM_ERR_INVALID_ARGUMENT, "%s is on device %d, the current device is %d", name,
                 a.device, dev);
   if (!aligned(p, align))
@@ -191,7 +196,7 @@ fathom_status check_on_device(const void *p, const char *name, size_t align) {
 
 #define REQUIRE_ON_DEVICE(ptr, name, align)                         \
   do {                                                              \
-    const fathom_status st_ = check_on_device((ptr), (name), (align)); \
+    const fathom_status st_ = check_on_device((ptr), (name), (align), dev); \
     if (st_ != FATHOM_OK) return st_;                               \
   } while (0)
 
@@ -223,7 +228,7 @@ fathom_status check_kv_shape(const fathom_kv_cache &c, const fathom_kv_batch &b)
   return FATHOM_OK;
 }
 
-fathom_status check_kv_pointers(const fathom_kv_cache &c, const fathom_kv_batch &b) {
+fathom_status check_kv_pointers(const fathom_kv_cache &c, const fathom_kv_batch &b, int dev) {
   REQUIRE_ON_DEVICE(c.k, "cache.k", 16);
   REQUIRE_ON_DEVICE(c.v, "cache.v", 16);
   if (c.dtype == FATHOM_E4M3) {
@@ -675,7 +680,8 @@ fathom_status fathom_kv_append(const fathom_kv_append_args *a, void *stream) {
           "rotary_pairs=%d out of range [0, d/2=%d]", a->rotary_pairs, d / 2);
   REQUIRE(a->rotary_pairs == 0 || a->inv_freq != nullptr, "inv_freq is NULL");
   if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return ok();
-  st = check_kv_pointers(a->cache, a->batch);
+  const int dev = current_device();
+  st = check_kv_pointers(a->cache, a->batch, dev);
   if (st != FATHOM_OK) return st;
   REQUIRE_ON_DEVICE(a->k, "k", elt_size(a->kv_dtype));
   REQUIRE_ON_DEVICE(a->v, "v", elt_size(a->kv_dtype));
@@ -710,7 +716,8 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   fathom_status st = check_kv_attention(a, p);
   if (st != FATHOM_OK) return st;
   if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return ok();
-  st = check_kv_pointers(a->cache, a->batch);
+  const int dev = current_device();
+  st = check_kv_pointers(a->cache, a->batch, dev);
   if (st != FATHOM_OK) return st;
   const size_t el = elt_size(a->q_dtype);
   REQUIRE_ON_DEVICE(a->q, "q", el);
@@ -726,6 +733,7 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   p.k_scale = a->cache.k_scale;
   p.v_scale = a->cache.v_scale;
   p.q = a->q;
+  p.q_wide = aligned(a->q, 16) && p.q_stride % (p.q_bf16 ? 8 : 4) == 0;
   p.out = a->out;
   p.lse = a->lse;
   unsigned char *base = static_cast<unsigned char *>(ws);

@@ -213,22 +213,89 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
   if (split > 0 && i0 >= tiles.count) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
-  // q's fragments: column g, this lane's dimensions
-  uint32_t qf[TERMS][kSteps][2];
-  float col_scale;  // of column g: softmax scale * log2 e, and q's power of two back
+  // this warp's tiles: number n is tile i0 + warp + kWarps n
+  const int mine = i1 - i0 - warp > 0 ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;
+  auto key_of = [&](int n) { return kKvBlock * tiles.at(i0 + warp + kWarps * n); };
+  // lane l looks up tile 32 batch + l: page, place and scales, far ahead of use
+  auto look = [&](int batch) {
+    Found x = {-1, 0, 0};
+    const int n = 32 * batch + lane;
+    if (n < mine) {
+      const int key = key_of(n);
+      const int at = (int)((unsigned)key / (unsigned)a.b.page_tokens);
+      x.page = kv_page(a.b, s, at);
+      x.slot = key - at * a.b.page_tokens;
+      if (F8 && x.page >= 0) {
+        const int64_t i = ((int64_t)x.page * a.b.h_kv + head) * (a.b.page_tokens / kKvBlock) +
+                          x.slot / kKvBlock;
+        x.scales = __ldg(a.k_scale + i) | (__ldg(a.v_scale + i) << 8);
+      }
+    }
+    return x;
+  };
+  Found cur = look(0), next = look(1);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) + warp * S::kDepth * S::kStage;
+  int batch = 0;  // of `cur`
+  // starts the copy of tile n (of batch or batch + 1) into its place in the ring
+  auto issue = [&](int n) {
+    if (n < mine) {
+      const bool here = n >> 5 == batch;
+      const int page = __shfl_sync(0xffffffffu, here ? cur.page : next.page, n & 31);
+      const int slot = __shfl_sync(0xffffffffu, here ? cur.slot : next.slot, n & 31);
+      if (page >= 0) {
+        const int64_t off = (((int64_t)page * a.b.h_kv + head) * a.b.page_tokens + slot) * S::kRow;
+        const uint32_t to = ring + n % S::kDepth * S::kStage;
+#pragma unroll
+        for (int u = 0; u < S::kRow / 32; ++u) {
+          const int i = lane + 32 * u, r = i / (S::kRow / 16), c = i % (S::kRow / 16);
+          const uint32_t dst = to + r * S::kPitch + c * 16;
+          tc_cp_async16(dst, static_cast<const uint8_t *>(a.ck) + off + i * 16, 16);
+          tc_cp_async16(dst + S::kSide, static_cast<const uint8_t *>(a.cv) + off + i * 16, 16);
+        }
+      }
+    }
+    tc_cp_async_commit();
+  };
+  // q: column g, this lane's dimensions.  Its loads and the first tiles' copies are
+  // on their way together.
+  float qv[4 * kSteps];
   {
     const int c = c0 + g;
-    float qv[4 * kSteps];
-    float big = 0.0f;
-    const int row = q.row0 + c / a.G, h = head * a.G + c % a.G;
+    const int64_t at = (int64_t)(q.row0 + c / a.G) * a.q_stride + (int64_t)(head * a.G + c % a.G) * D;
+    constexpr int kPiece = S::kKVec / S::kElt;  // dimensions that follow each other
+    const bool wide = a.q_wide;
 #pragma unroll
-    for (int e = 0; e < 4 * kSteps; ++e) {
-      qv[e] = c < c1 ? load_q(a.q, a.q_bf16, (int64_t)row * a.q_stride + (int64_t)h * D + S::k_dim(e, t))
-                     : 0.0f;
-      big = fmaxf(big, fabsf(qv[e]));
+    for (int e = 0; e < 4 * kSteps; e += kPiece) {
+      const int64_t i = at + S::k_dim(e, t);
+#pragma unroll
+      for (int w = 0; w < kPiece; ++w) qv[e + w] = 0.0f;
+      if (c < c1) {
+        if (wide && a.q_bf16) {
+#pragma unroll
+          for (int w = 0; w < kPiece; w += 8) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + i + w));
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              qv[e + w + z] = __uint_as_float(z & 1 ? y[z / 2] & 0xffff0000u : y[z / 2] << 16);
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < kPiece; ++w) qv[e + w] = load_q(a.q, a.q_bf16, i + w);
+        }
+      }
     }
-    col_scale = a.qscale;
+  }
+#pragma unroll
+  for (int n = 0; n < S::kDepth - 1; ++n) issue(n);
+
+  uint32_t qf[TERMS][kSteps][2];
+  float col_scale = a.qscale;  // of column g: softmax scale * log2 e, and q's power of two back
+  {
     if constexpr (F8) {
+      float big = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4 * kSteps; ++e) big = fmaxf(big, fabsf(qv[e]));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
       // big to [2^14, 2^15): exact, and 28 binades below stay normal
@@ -358,51 +425,6 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
     }
   };
 
-  // this warp's tiles: number n is tile i0 + warp + kWarps n
-  const int mine = i1 - i0 - warp > 0 ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;
-  auto key_of = [&](int n) { return kKvBlock * tiles.at(i0 + warp + kWarps * n); };
-  // lane l looks up tile 32 batch + l: page, place and scales, far ahead of use
-  auto look = [&](int batch) {
-    Found x = {-1, 0, 0};
-    const int n = 32 * batch + lane;
-    if (n < mine) {
-      const int key = key_of(n);
-      const int at = (int)((unsigned)key / (unsigned)a.b.page_tokens);
-      x.page = kv_page(a.b, s, at);
-      x.slot = key - at * a.b.page_tokens;
-      if (F8 && x.page >= 0) {
-        const int64_t i = ((int64_t)x.page * a.b.h_kv + head) * (a.b.page_tokens / kKvBlock) +
-                          x.slot / kKvBlock;
-        x.scales = __ldg(a.k_scale + i) | (__ldg(a.v_scale + i) << 8);
-      }
-    }
-    return x;
-  };
-  Found cur = look(0), next = look(1);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) + warp * S::kDepth * S::kStage;
-  int batch = 0;  // of `cur`
-  // starts the copy of tile n (of batch or batch + 1) into its place in the ring
-  auto issue = [&](int n) {
-    if (n < mine) {
-      const bool here = n >> 5 == batch;
-      const int page = __shfl_sync(0xffffffffu, here ? cur.page : next.page, n & 31);
-      const int slot = __shfl_sync(0xffffffffu, here ? cur.slot : next.slot, n & 31);
-      if (page >= 0) {
-        const int64_t off = (((int64_t)page * a.b.h_kv + head) * a.b.page_tokens + slot) * S::kRow;
-        const uint32_t to = ring + n % S::kDepth * S::kStage;
-#pragma unroll
-        for (int u = 0; u < S::kRow / 32; ++u) {
-          const int i = lane + 32 * u, r = i / (S::kRow / 16), c = i % (S::kRow / 16);
-          const uint32_t dst = to + r * S::kPitch + c * 16;
-          tc_cp_async16(dst, static_cast<const uint8_t *>(a.ck) + off + i * 16, 16);
-          tc_cp_async16(dst + S::kSide, static_cast<const uint8_t *>(a.cv) + off + i * 16, 16);
-        }
-      }
-    }
-    tc_cp_async_commit();
-  };
-#pragma unroll
-  for (int n = 0; n < S::kDepth - 1; ++n) issue(n);
   for (int n = 0; n < mine; ++n) {
     if (n >> 5 != batch) {
       batch = n >> 5;
@@ -585,9 +607,11 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, fl
 template <int D, bool F8, typename Kernel>
 cudaError_t launch_ring(Kernel kernel, int64_t blocks, const KvAttnParams &a, cudaStream_t s) {
   constexpr int smem = Shape<D, F8>::kSmem;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, s, a);
 }
 
@@ -659,10 +683,12 @@ void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
   // the most tiles that one unit's columns can see
   const int64_t tokens = (a.cols + a.G - 2) / a.G + 1;  // tokens that `cols` columns can span
   int64_t most = ((int64_t)a.b.max_len + a.tile - 1) / a.tile;
+  bool windowed = false;
   if (a.window < a.b.max_len) {
     const int64_t w = ((int64_t)a.window + tokens - 1 + a.tile - 2) / a.tile + 1 +
                       ((int64_t)a.sinks + a.tile - 1) / a.tile;
-    if (w < most) most = w;
+    windowed = w < most;
+    if (windowed) most = w;
   }
   if (most < 1) most = 1;
   const int64_t base = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles;
@@ -672,8 +698,14 @@ void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
     splits = 148 / ((int64_t)a.pairs * a.col_tiles);
     if (splits > most / 8) splits = most / 8;
   } else {
-    // as many blocks as the SMs hold at once, and at least 4 tiles a warp
-    const int64_t want = kv_resident_blocks(d, f8) / base > 0 ? kv_resident_blocks(d, f8) / base : 1;
+    // Runs of at least 4 tiles a warp.  Where every sequence goes through about the
+    // same number of tiles (a window), as many blocks as the SMs hold at once; where
+    // lengths differ from the bound and from each other, smaller runs, so that the
+    // SMs end together (24 sessions of 4096 to 65536 tokens: 501 us with one block
+    // a place, 357 with 2, 309 with 4, 292 with 8; one session, 64 windowed ones: 1
+    // to 4 are within 1%, 8 costs 2 and 6%).
+    const int64_t waves = windowed ? 1 : a.b.num_seqs > 1 ? 8 : 4;
+    const int64_t want = (waves * kv_resident_blocks(d, f8) + base - 1) / base;
     splits = most / (4 * kWarps);
     if (splits > want) splits = want;
   }

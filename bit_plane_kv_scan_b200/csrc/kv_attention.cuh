@@ -19,6 +19,7 @@ struct KvAttnParams {
   const void *q;
   int64_t q_stride;
   int q_bf16;  // and out's type
+  int q_wide;  // 16-byte loads of q's rows are aligned
   int h_q, G;
   float qscale;       // softmax scale * log2(e)
   int window, sinks;  // window: above max_len where there is none

@@ -315,13 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint16_t *src = static_cast<const uint16_t *>(a.q) +
                               (int64_t)(q.row0 + c / a.G) * a.q_stride +
                               (int64_t)(head * a.G + c % a.G) * D;
-        const bool wide = ((uintptr_t)a.q & 15) == 0 && a.q_stride % 8 == 0;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           uint4 x = make_uint4(0, 0, 0, 0);
           if (c < c1) {
             const uint16_t *e = src + 8 * i;
-            if (wide) {
+            if (a.q_wide) {
               x = *reinterpret_cast<const uint4 *>(e);
             } else {
               x.x = e[0] | ((uint32_t)e[1] << 16);

@@ -590,6 +590,7 @@ class KVCache:
             raise ValueError("the cache's tensors must be contiguous")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.device
+        self.h_kv, self.page_tokens, self.d = h_kv, tokens, d
         self.args = KvCacheArgs(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
                                 dtype=BF16 if k.dtype == torch.bfloat16 else E4M3, num_pages=pages,
                                 page_tokens=tokens, h_kv=h_kv, d=d)
@@ -641,14 +642,21 @@ class KVBatch:
         self.num_rows, self.max_rows, self.max_len = rows, int(max_rows), max_len
         self.device = page_table.device
 
+        self._args = {}  # by the cache's page_tokens, which the default max_len follows
+
     def args_for(self, cache: KVCache) -> KvBatchArgs:
+        page_tokens = cache.page_tokens
+        got = self._args.get(page_tokens)
+        if got is not None:
+            return got
         most = self.max_len
         if most is None:
-            most = min(self.page_table.shape[1] * cache.args.page_tokens, KV_MAX_LEN)
-        return KvBatchArgs(page_table=_ptr(self.page_table), seq_len=_ptr(self.seq_len),
+            most = min(self.page_table.shape[1] * page_tokens, KV_MAX_LEN)
+        got = self._args[page_tokens] = KvBatchArgs(page_table=_ptr(self.page_table), seq_len=_ptr(self.seq_len),
                            q_start=_ptr(self.q_start), num_seqs=self.page_table.shape[0],
                            table_width=self.page_table.shape[1], num_rows=self.num_rows,
                            max_rows=self.max_rows, max_len=int(most))
+        return got
 
 
 def _same_device(*tensors: torch.Tensor) -> torch.device:
@@ -661,24 +669,49 @@ def _same_device(*tensors: torch.Tensor) -> torch.device:
 
 def _rows_of(x: torch.Tensor, name: str, rows: int, d: int) -> int:
     """The row stride of [rows, heads, d] rows whose heads are contiguous."""
-    if x.dim() != 3 or x.shape[0] != rows or x.shape[2] != d:
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != d:
         raise ValueError("%s must be [num_rows=%d, heads, d=%d]" % (name, rows, d))
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d)):
+    row, head, one = x.stride()
+    if (one != 1 or (head != d and shape[1] > 1)) and x.numel():
         raise ValueError("%s: each row's heads must be contiguous" % name)
-    return x.stride(0) if rows > 1 else 0
+    return row if rows > 1 else 0
 
 
-def _launch_stream(stream, device: torch.device):
-    return torch.cuda.current_stream(device) if stream is None else stream
+def _on(device: torch.device, *tensors: Optional[torch.Tensor]):
+    for x in tensors:
+        if x is not None and x.device != device:
+            raise ValueError("tensors on %s and %s" % (device, x.device))
 
 
-def _hold(stream, device: torch.device, *tensors):
-    """Memory that torch allocated for its current stream but that `stream` uses:
-    the allocator must not hand it out again before `stream` has passed."""
-    if stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
-        for x in tensors:
-            if x is not None:
-                x.record_stream(stream)
+class _Launch:
+    """The current device and stream of a call on `device`.  `hold` is for memory that
+    torch allocated for its current stream but that another stream uses: the
+    allocator must not hand it out again before that stream has passed."""
+
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
+            raise ValueError("the cache is on %s, not on a CUDA device" % device)
+        self.guard = None
+        if torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+            self.guard.__enter__()
+        current = torch.cuda.current_stream()
+        self.stream = current if stream is None else stream
+        self.raw = self.stream.cuda_stream
+        self.other = stream is not None and self.raw != current.cuda_stream
+
+    def hold(self, x: torch.Tensor) -> torch.Tensor:
+        if self.other:
+            x.record_stream(self.stream)
+        return x
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, *,
@@ -691,31 +724,28 @@ def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, 
     (None: no rotation); pair r is dimensions r and r + pairs, or 2r and 2r + 1 with
     interleaved.  Rows may be strided (parts of a fused projection).  Returns the
     rotated q [num_rows, h_q, d] (None without q); q_out=q rotates in place."""
-    c = cache.args
-    _same_device(cache.k, batch.page_table, k, v, *(x for x in (q, inv_freq, q_out) if x is not None))
-    ks, vs = _rows_of(k, "k", batch.num_rows, c.d), _rows_of(v, "v", batch.num_rows, c.d)
-    if k.shape[1] != c.h_kv or v.shape[1] != c.h_kv or v.dtype != k.dtype:
-        raise ValueError("k and v must both be [num_rows, h_kv=%d, d] of one dtype" % c.h_kv)
+    device, rows, d = cache.device, batch.num_rows, cache.d
+    _on(device, batch.page_table, k, v, q, inv_freq, q_out)
+    ks, vs = _rows_of(k, "k", rows, d), _rows_of(v, "v", rows, d)
+    if k.shape[1] != cache.h_kv or v.shape[1] != cache.h_kv or v.dtype != k.dtype:
+        raise ValueError("k and v must both be [num_rows, h_kv=%d, d] of one dtype" % cache.h_kv)
     pairs = 0
     if inv_freq is not None:
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise TypeError("inv_freq must be a contiguous float32 [pairs] tensor")
         pairs = inv_freq.shape[0]
-    a = KvAppendArgs(cache=c, batch=batch.args_for(cache), k=_ptr(k), v=_ptr(v),
-                     kv_dtype=_dtype_code(k), k_stride=ks, v_stride=vs,
-                     inv_freq=_ptr(inv_freq) if pairs else None, rotary_pairs=pairs,
-                     interleaved=int(interleaved))
-    with torch.cuda.device(cache.device):
-        stream = _launch_stream(stream, cache.device)
+    a = KvAppendArgs(cache.args, batch.args_for(cache), k.data_ptr(), v.data_ptr(), _dtype_code(k), ks, vs)
+    if pairs:
+        a.inv_freq, a.rotary_pairs, a.interleaved = inv_freq.data_ptr(), pairs, int(interleaved)
+    with _Launch(device, stream) as at:
         if q is not None:
-            a.q_stride = _rows_of(q, "q", batch.num_rows, c.d)
+            a.q_stride = _rows_of(q, "q", rows, d)
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-                _hold(stream, cache.device, q_out)
+                q_out = at.hold(q.new_empty(q.shape))
             elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and dtype")
-            a.q, a.q_out, a.q_dtype, a.h_q = _ptr(q), _ptr(q_out), _dtype_code(q), q.shape[1]
-        _check(lib().fathom_kv_append(ctypes.byref(a), ctypes.c_void_p(stream.cuda_stream)))
+            a.q, a.q_out, a.q_dtype, a.h_q = q.data_ptr(), q_out.data_ptr(), _dtype_code(q), q.shape[1]
+        _check(lib().fathom_kv_append(ctypes.byref(a), at.raw))
     return q_out if q is not None else None
 
 
@@ -730,34 +760,29 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
     Returns (out [num_rows, h_q, d] of q's dtype, lse f32 [num_rows, h_q]); rows that
     no sequence has are left as they were.  Without a workspace the call takes
     one from torch's allocator, so that two captured graphs never share one."""
-    c = cache.args
-    _same_device(cache.k, batch.page_table, q, *(x for x in (out, lse) if x is not None))
-    qs = _rows_of(q, "q", batch.num_rows, c.d)
+    device, rows, d = cache.device, batch.num_rows, cache.d
+    _on(device, batch.page_table, q, out, lse)
+    qs = _rows_of(q, "q", rows, d)
     if softmax_scale is None:
-        softmax_scale = 1.0 / float(c.d) ** 0.5
-    a = KvAttentionArgs(cache=c, batch=batch.args_for(cache), q=_ptr(q), q_dtype=_dtype_code(q),
-                        h_q=q.shape[1], q_stride=qs, softmax_scale=float(softmax_scale),
-                        window=int(window), sinks=int(sinks))
+        softmax_scale = 1.0 / float(d) ** 0.5
+    h_q = q.shape[1]
     L = lib()
-    with torch.cuda.device(cache.device):
-        stream = _launch_stream(stream, cache.device)
+    with _Launch(device, stream) as at:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _hold(stream, cache.device, out)
+            out = at.hold(q.new_empty(q.shape))
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and dtype")
         if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-            _hold(stream, cache.device, lse)
-        elif lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
+            lse = at.hold(q.new_empty((rows, h_q), dtype=torch.float32))
+        elif tuple(lse.shape) != (rows, h_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [num_rows, h_q]")
-        a.out, a.lse = _ptr(out), _ptr(lse)
-        need = L.fathom_kv_attention_workspace_size(ctypes.byref(a))
+        a = KvAttentionArgs(cache.args, batch.args_for(cache), q.data_ptr(), _dtype_code(q), h_q, qs,
+                            float(softmax_scale), int(window), int(sinks), out.data_ptr(), lse.data_ptr())
+        ref = ctypes.byref(a)
+        need = L.fathom_kv_attention_workspace_size(ref)
         if workspace is None:
-            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
-            _hold(stream, cache.device, ws)
+            ws = at.hold(q.new_empty((max(need, 1),), dtype=torch.uint8))
         else:
             ws = workspace.get(need)
-        _check(L.fathom_kv_attention(ctypes.byref(a), _ptr(ws), need,
-                                     ctypes.c_void_p(stream.cuda_stream)))
+        _check(L.fathom_kv_attention(ref, ws.data_ptr(), need, at.raw))
     return out, lse
