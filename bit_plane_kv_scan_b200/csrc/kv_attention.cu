@@ -131,7 +131,7 @@ struct Shape {
   // (an odd number of 16-byte pieces: the pieces that 8 lanes read at once lie
   // in different banks).
   static constexpr int kPitch = kRow + 16, kSide = kKvBlock * kPitch, kStage = 2 * kSide;
-  static constexpr int kDepth = kRow <= 64 ? 6 : kRow <= 128 ? 4 : 3;
+  static constexpr int kDepth = 3;
   static constexpr int kSmem = kWarps * kDepth * kStage;
   // The byte of piece j of the lane's part of a K row: two neighbouring pieces of
   // 128 bytes, so that four lanes' pieces 0 are every second one.
@@ -486,7 +486,8 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
 }
 
 template <int D, bool F8, int TERMS>
-__global__ void __launch_bounds__(kThreads) kv_attention_kernel(KvAttnParams a) {
+__global__ void __launch_bounds__(kThreads, F8 && TERMS == 1 && D <= 128 ? 4 : 1)
+    kv_attention_kernel(KvAttnParams a) {
   grid_dependency_wait();
   allow_dependent_launch();
   if (blockIdx.x == gridDim.x - 1) {
@@ -650,8 +651,8 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
 // Blocks of the few-rows kernel that the device holds at once, by shared memory
 // (228 KB an SM, 1 KB of it for each block).
 static int kv_resident_blocks(int d, bool f8) {
-  const int row = f8 ? d : 2 * d, depth = row <= 64 ? 6 : row <= 128 ? 4 : 3;
-  const int smem = kWarps * depth * 2 * kKvBlock * (row + 16) + 1280;
+  const int row = f8 ? d : 2 * d;
+  const int smem = kWarps * 3 * 2 * kKvBlock * (row + 16) + 1280;
   const int per = 228 * 1024 / smem;
   return 148 * (per > 4 ? 4 : per);
 }
