@@ -156,6 +156,8 @@ _lock = threading.Lock()
 def lib() -> ctypes.CDLL:
     """Load libfathom.so; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -685,24 +687,31 @@ def _on(device: torch.device, *tensors: Optional[torch.Tensor]):
 
 
 class _Launch:
-    """The current device and stream of a call on `device`.  `hold` is for memory that
-    torch allocated for its current stream but that another stream uses: the
-    allocator must not hand it out again before that stream has passed."""
+    """The current device and stream of a call on a cache's device.  `new` allocates as
+    torch does, for its current stream; where the call goes to another stream, the
+    allocator is told not to hand the memory out again before that stream has passed."""
+
+    __slots__ = ("guard", "stream", "raw")
 
     def __init__(self, device: torch.device, stream):
         if device.type != "cuda":
             raise ValueError("the cache is on %s, not on a CUDA device" % device)
         self.guard = None
-        if torch.cuda.current_device() != device.index:
+        if torch._C._cuda_getDevice() != device.index:
             self.guard = torch.cuda.device(device)
             self.guard.__enter__()
-        current = torch.cuda.current_stream()
-        self.stream = current if stream is None else stream
-        self.raw = self.stream.cuda_stream
-        self.other = stream is not None and self.raw != current.cuda_stream
+        # the handle alone: torch.cuda.current_stream() makes an object around it
+        self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+        self.stream = None
+        if stream is not None and stream.cuda_stream != self.raw:
+            self.stream, self.raw = stream, stream.cuda_stream
 
-    def hold(self, x: torch.Tensor) -> torch.Tensor:
-        if self.other:
+    def new(self, like: torch.Tensor, shape=None, dtype=None) -> torch.Tensor:
+        if shape is None and like.is_contiguous():
+            x = torch.empty_like(like)
+        else:
+            x = like.new_empty(like.shape if shape is None else shape, dtype=dtype)
+        if self.stream is not None:
             x.record_stream(self.stream)
         return x
 
@@ -741,7 +750,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, 
         if q is not None:
             a.q_stride = _rows_of(q, "q", rows, d)
             if q_out is None:
-                q_out = at.hold(q.new_empty(q.shape))
+                q_out = at.new(q)
             elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and dtype")
             a.q, a.q_out, a.q_dtype, a.h_q = q.data_ptr(), q_out.data_ptr(), _dtype_code(q), q.shape[1]
@@ -769,11 +778,11 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
     L = lib()
     with _Launch(device, stream) as at:
         if out is None:
-            out = at.hold(q.new_empty(q.shape))
+            out = at.new(q)
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and dtype")
         if lse is None:
-            lse = at.hold(q.new_empty((rows, h_q), dtype=torch.float32))
+            lse = at.new(q, (rows, h_q), torch.float32)
         elif tuple(lse.shape) != (rows, h_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [num_rows, h_q]")
         a = KvAttentionArgs(cache.args, batch.args_for(cache), q.data_ptr(), _dtype_code(q), h_q, qs,
@@ -781,7 +790,7 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
         ref = ctypes.byref(a)
         need = L.fathom_kv_attention_workspace_size(ref)
         if workspace is None:
-            ws = at.hold(q.new_empty((max(need, 1),), dtype=torch.uint8))
+            ws = at.new(q, (max(need, 1),), torch.uint8)
         else:
             ws = workspace.get(need)
         _check(L.fathom_kv_attention(ref, ws.data_ptr(), need, at.raw))
