@@ -3,14 +3,19 @@
 //
 // Row at position p, pair r: angle a = p f_r, (x, y) -> (x cos a - y sin a,
 // y cos a + x sin a).  The angle is formed and reduced to [-pi, pi] in fp64 (in
-// fp32 a position of a million turns by a wrong 0.06), then sincosf.  A
-// block of threads shares one row's sines and cosines between all its heads.
+// fp32 a position of a million turns by a wrong 0.06), then sincosf.
+//
+// A unit is the rows of one sequence that fall into one block of 16 positions.
+// Its first thread block takes keys and values, the others `q_heads` query heads
+// each; each works out the unit's sines and cosines for itself (1024 of them at
+// d = 128, against 32768 elements or more) and keeps them in shared memory.
 //
 // An E4M3 cache has a power-of-two scale per block of 16 tokens and KV head, so
 // a whole block belongs to one warp: it finds the largest new element, raises
 // the scale if it must, moves the codes that the block already held, and writes
-// the new ones.  The scale comes from the elements before the rotation, which
-// makes it the same whatever the sines' last bit, and leaves room for sqrt 2.
+// the new ones (it reads its rows twice, the second time from L1).  The scale
+// comes from the elements before the rotation, which makes it the same whatever
+// the sines' last bit, and leaves room for sqrt 2.
 //
 // Bound by bytes: every element is read and written once.
 #include <cuda_bf16.h>
@@ -25,7 +30,8 @@ constexpr int kAppendThreads = 32 * kAppendWarps;
 
 struct AppendParams {
   KvBatch b;
-  int d, G, h_q;
+  int d, h_q;          // (h_q: 0 without queries)
+  int q_heads, parts;  // query heads of a thread block, thread blocks of a unit
   void *ck, *cv;
   uint8_t *k_scale, *v_scale;
   const void *k, *v, *q;
@@ -124,7 +130,7 @@ __device__ __forceinline__ void rotate_task(const T *head, int t, int d, int pai
 
 // Tasks of one head: pairs W at a time, then the elements that stay.
 template <int W>
-__device__ __forceinline__ int rotate_tasks(int d, int pairs, int interleaved) {
+__host__ __device__ __forceinline__ int rotate_tasks(int d, int pairs, int interleaved) {
   return (interleaved && W > 1 ? 2 * pairs / W : pairs / W) + (d - 2 * pairs) / W;
 }
 
@@ -134,65 +140,6 @@ __device__ __forceinline__ void store_vec(T *at, const float *o) {
 #pragma unroll
   for (int i = 0; i < W; ++i) v.x[i] = from_float<T>(o[i]);
   *reinterpret_cast<Vec<T, W> *>(at) = v;
-}
-
-// The queries of one row, by the whole thread block (`tid` of `nt` threads).
-template <int W, typename TQ>
-__device__ __forceinline__ void rotate_queries(const AppendParams &p, int row, const float2 *cs,
-                                               int tid, int nt) {
-  const int per = rotate_tasks<W>(p.d, p.pairs, p.interleaved);
-  const TQ *src = static_cast<const TQ *>(p.q) + (int64_t)row * p.q_stride;
-  TQ *dst = static_cast<TQ *>(p.q_out) + (int64_t)row * p.h_q * p.d;
-  for (int i = tid; i < p.h_q * per; i += nt) {
-    const int h = i / per, t = i - h * per;
-    TQ *out = dst + (int64_t)h * p.d;
-    rotate_task<W>(src + (int64_t)h * p.d, t, p.d, p.pairs, p.interleaved, cs,
-                   [&](int at, const float *o, const float *) { store_vec<W>(out + at, o); });
-  }
-}
-
-// bf16 cache: one thread block per row.
-template <int W, typename TKV, typename TQ>
-__global__ void __launch_bounds__(kAppendThreads) append_bf16_kernel(AppendParams p) {
-  grid_dependency_wait();
-  allow_dependent_launch();
-  __shared__ float2 cs[FATHOM_MAX_D / 2];
-  const int row = blockIdx.x;
-  const int s = p.b.q_start ? find_seq(p.b.num_seqs, row, [&](int i) { return p.b.q_start[i]; }) : row;
-  const KvSeq q = kv_seq(p.b, s);
-  if (row < q.row0 || row >= q.row0 + q.rows) return;  // no sequence has this row
-  const int pos = q.len - q.rows + (row - q.row0);
-  for (int r = threadIdx.x; r < p.pairs; r += kAppendThreads) cs[r] = cos_sin(pos, p.inv_freq[r]);
-  __syncthreads();
-  if (p.q) rotate_queries<W, TQ>(p, row, cs, threadIdx.x, kAppendThreads);
-  if (pos < 0) return;
-  const int page = kv_page(p.b, s, pos / p.b.page_tokens);
-  if (page < 0) return;
-  const int slot = pos % p.b.page_tokens;
-  const int d = p.d;
-  const int per_k = rotate_tasks<W>(d, p.pairs, p.interleaved), per_v = d / W;
-  const TKV *k = static_cast<const TKV *>(p.k) + (int64_t)row * p.k_stride;
-  const TKV *v = static_cast<const TKV *>(p.v) + (int64_t)row * p.v_stride;
-  auto at = [&](void *base, int g) {
-    return static_cast<__nv_bfloat16 *>(base) +
-           (((int64_t)page * p.b.h_kv + g) * p.b.page_tokens + slot) * d;
-  };
-  const int n_k = p.b.h_kv * per_k, n_v = p.b.h_kv * per_v;
-  for (int i = threadIdx.x; i < n_k + n_v; i += kAppendThreads) {
-    if (i < n_k) {
-      const int g = i / per_k, t = i - g * per_k;
-      __nv_bfloat16 *out = at(p.ck, g);
-      rotate_task<W>(k + (int64_t)g * d, t, d, p.pairs, p.interleaved, cs,
-                     [&](int c, const float *o, const float *) { store_vec<W>(out + c, o); });
-    } else {
-      const int g = (i - n_k) / per_v, t = (i - n_k) - g * per_v;
-      const Vec<TKV, W> x = *reinterpret_cast<const Vec<TKV, W> *>(v + (int64_t)g * d + t * W);
-      float o[W];
-#pragma unroll
-      for (int e = 0; e < W; ++e) o[e] = to_float(x.x[e]);
-      store_vec<W>(at(p.cv, g) + t * W, o);
-    }
-  }
 }
 
 // The smallest exponent byte whose scale holds |x| <= big within 256.
@@ -213,18 +160,27 @@ __device__ __forceinline__ float e4m3_float(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }
 
-// E4M3 cache: one thread block per block of 16 tokens of a sequence (unit), a
-// warp per KV head and side.  A sequence's m rows touch at most m / 16 + 2
-// blocks, so the units of sequence s start at q_start[s] / 16 + 2 s.
-template <int W, typename TKV, typename TQ>
-__global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(AppendParams p) {
+// Rows m of a unit, `heads` heads each of `per` tasks, by the whole thread block:
+// fn(row, head, task).
+template <typename Fn>
+__device__ __forceinline__ void for_tasks(int m, int heads, int per, Fn fn) {
+  const int n = m * heads * per;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kAppendThreads) {
+    const int t = i % per, rh = i / per;
+    fn(rh / heads, rh % heads, t);
+  }
+}
+
+// A sequence's m rows touch at most m / 16 + 2 blocks of positions, so the units
+// of sequence s start at q_start[s] / 16 + 2 s.
+template <int W, typename TKV, typename TQ, bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
-  extern __shared__ float smem[];
+  extern __shared__ float2 cs[];  // [16][pairs]
   const int d = p.d;
-  float2 *cs = reinterpret_cast<float2 *>(smem);             // [16][pairs]
-  float *stage = smem + 2 * kKvBlock * p.pairs;              // [warps][16][d]
-  const int unit = blockIdx.x;
+  const int unit = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   int s = unit, u = 0;
   if (p.b.q_start) {
     auto base = [&](int i) { return (int64_t)(p.b.q_start[i] >> 4) + 2 * (int64_t)i; };
@@ -241,80 +197,117 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(AppendParam
   for (int i = threadIdx.x; i < m * p.pairs; i += kAppendThreads)
     cs[i] = cos_sin(p0 + i / p.pairs, p.inv_freq[i % p.pairs]);
   __syncthreads();
-  if (p.q)
-    for (int r = 0; r < m; ++r)
-      rotate_queries<W, TQ>(p, row0 + r, cs + r * p.pairs, threadIdx.x, kAppendThreads);
+
+  if (part > 0) {  // queries
+    const int h0 = (part - 1) * p.q_heads, heads = min(p.q_heads, p.h_q - h0);
+    const TQ *src = static_cast<const TQ *>(p.q) + (int64_t)row0 * p.q_stride + (int64_t)h0 * d;
+    TQ *dst = static_cast<TQ *>(p.q_out) + ((int64_t)row0 * p.h_q + h0) * d;
+    for_tasks(m, heads, rotate_tasks<W>(d, p.pairs, p.interleaved), [&](int r, int h, int t) {
+      TQ *out = dst + ((int64_t)r * p.h_q + h) * d;
+      rotate_task<W>(src + r * p.q_stride + h * d, t, d, p.pairs, p.interleaved, cs + r * p.pairs,
+                     [&](int at, const float *o, const float *) { store_vec<W>(out + at, o); });
+    });
+    return;
+  }
   if (blk < 0) return;
   const int page = kv_page(p.b, s, blk * kKvBlock / p.b.page_tokens);
   if (page < 0) return;
-  const int slot0 = blk * kKvBlock % p.b.page_tokens;  // the block's first row in its page
-  const int held = p0 - blk * kKvBlock;                // tokens the block has from before
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *st = stage + warp * kKvBlock * d;
-  for (int i = warp; i < 2 * p.b.h_kv; i += kAppendWarps) {
-    const bool is_v = i >= p.b.h_kv;
-    const int g = is_v ? i - p.b.h_kv : i;
-    const TKV *src = static_cast<const TKV *>(is_v ? p.v : p.k) +
-                     (int64_t)row0 * (is_v ? p.v_stride : p.k_stride) + (int64_t)g * d;
-    const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    const int pairs = is_v ? 0 : p.pairs;
-    const int per = rotate_tasks<W>(d, pairs, p.interleaved && !is_v);
-    float big = 0.0f;
-    for (int t = lane; t < m * per; t += 32) {
-      const int r = t / per;
-      rotate_task<W>(src + r * stride, t - r * per, d, pairs, is_v ? 0 : p.interleaved,
-                     cs + r * p.pairs, [&](int at, const float *o, const float *raw) {
+  const int held = p0 - blk * kKvBlock;                         // tokens the block has from before
+  const int slot0 = blk * kKvBlock % p.b.page_tokens;           // the block's first row in its page
+  const int64_t head0 = (int64_t)page * p.b.h_kv;
+  const TKV *k = static_cast<const TKV *>(p.k) + (int64_t)row0 * p.k_stride;
+  const TKV *v = static_cast<const TKV *>(p.v) + (int64_t)row0 * p.v_stride;
+  const int per_k = rotate_tasks<W>(d, p.pairs, p.interleaved), per_v = d / W;
+
+  if constexpr (!E4M3) {
+    auto place = [&](void *base, int r, int g) {
+      return static_cast<__nv_bfloat16 *>(base) +
+             ((head0 + g) * p.b.page_tokens + slot0 + held + r) * d;
+    };
+    for_tasks(m, p.b.h_kv, per_k, [&](int r, int g, int t) {
+      __nv_bfloat16 *out = place(p.ck, r, g);
+      rotate_task<W>(k + r * p.k_stride + g * d, t, d, p.pairs, p.interleaved, cs + r * p.pairs,
+                     [&](int at, const float *o, const float *) { store_vec<W>(out + at, o); });
+    });
+    for_tasks(m, p.b.h_kv, per_v, [&](int r, int g, int t) {
+      rotate_task<W>(v + r * p.v_stride + g * d, t, d, 0, 0, cs,
+                     [&](int at, const float *o, const float *) { store_vec<W>(place(p.cv, r, g) + at, o); });
+    });
+    return;
+  } else {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = warp; i < 2 * p.b.h_kv; i += kAppendWarps) {
+      const bool is_v = i >= p.b.h_kv;
+      const int g = is_v ? i - p.b.h_kv : i;
+      const TKV *src = (is_v ? v : k) + g * d;
+      const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      const int64_t head = head0 + g;
+      uint8_t *scale = (is_v ? p.v_scale : p.k_scale) + head * (p.b.page_tokens / kKvBlock) +
+                       slot0 / kKvBlock;
+      uint8_t *codes = static_cast<uint8_t *>(is_v ? p.cv : p.ck) + (head * p.b.page_tokens + slot0) * d;
+      const int was = held ? kv_scale_exp(*scale) + 127 : 0;
+      float big = 0.0f;
+#pragma unroll 4
+      for (int t = lane; t < m * per_v; t += 32) {
+        const int r = t / per_v;
+        const Vec<TKV, W> x = *reinterpret_cast<const Vec<TKV, W> *>(src + r * stride + (t - r * per_v) * W);
 #pragma unroll
-                       for (int e = 0; e < W; ++e) {
-                         st[r * d + at + e] = o[e];
-                         if (fabsf(raw[e]) < INFINITY) big = fmaxf(big, fabsf(raw[e]));
-                       }
-                     });
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-    __syncwarp();
-    const int64_t head = (int64_t)page * p.b.h_kv + g;
-    uint8_t *scale = (is_v ? p.v_scale : p.k_scale) + head * (p.b.page_tokens / kKvBlock) +
-                     slot0 / kKvBlock;
-    uint32_t *codes = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(is_v ? p.cv : p.ck) +
-                                                   (head * p.b.page_tokens + slot0) * d);
-    int x = scale_byte(big);
-    if (held) {
-      const int was = kv_scale_exp(*scale) + 127;
-      if (x > was) {  // the older codes move to the larger scale
-        const float f = x - was > 126 ? 0.0f : exp2i(was - x);
-        for (int t = lane; t < held * d / 4; t += 32) {
-          const uint32_t c = codes[t];
-          codes[t] = pack_e4m3(e4m3_float(c & 255) * f, e4m3_float((c >> 8) & 255) * f,
-                               e4m3_float((c >> 16) & 255) * f, e4m3_float(c >> 24) * f);
+        for (int e = 0; e < W; ++e) {
+          const float y = fabsf(to_float(x.x[e]));
+          if (y < INFINITY) big = fmaxf(big, y);
         }
-      } else {
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+      int x = scale_byte(big);
+      if (held && x > was) {  // the older codes move to the larger scale
+        const float f = x - was > 126 ? 0.0f : exp2i(was - x);
+        uint32_t *c4 = reinterpret_cast<uint32_t *>(codes);
+        for (int t = lane; t < held * d / 4; t += 32) {
+          const uint32_t c = c4[t];
+          c4[t] = pack_e4m3(e4m3_float(c & 255) * f, e4m3_float((c >> 8) & 255) * f,
+                            e4m3_float((c >> 16) & 255) * f, e4m3_float(c >> 24) * f);
+        }
+      } else if (held) {
         x = was;
       }
+      const float f = exp2i(127 - x);
+      uint8_t *out = codes + held * d;
+      const int per = is_v ? per_v : per_k, pairs = is_v ? 0 : p.pairs;
+#pragma unroll 4
+      for (int t = lane; t < m * per; t += 32) {
+        const int r = t / per;
+        rotate_task<W>(src + r * stride, t - r * per, d, pairs, is_v ? 0 : p.interleaved,
+                       cs + r * p.pairs, [&](int at, const float *o, const float *) {
+                         uint8_t *to = out + r * d + at;
+                         if constexpr (W == 8)
+                           *reinterpret_cast<uint2 *>(to) =
+                               make_uint2(pack_e4m3(o[0] * f, o[1] * f, o[2] * f, o[3] * f),
+                                          pack_e4m3(o[4] * f, o[5] * f, o[6] * f, o[7] * f));
+                         else
+                           *to = (uint8_t)__nv_cvt_float_to_fp8(o[0] * f, __NV_SATFINITE, __NV_E4M3);
+                       });
+      }
+      if (lane == 0) *scale = (uint8_t)x;
     }
-    const float f = exp2i(127 - x);
-    for (int t = lane; t < m * d / 4; t += 32) {
-      const float4 o = *reinterpret_cast<const float4 *>(st + 4 * t);
-      codes[held * d / 4 + t] = pack_e4m3(o.x * f, o.y * f, o.z * f, o.w * f);
-    }
-    __syncwarp();
-    if (lane == 0) *scale = (uint8_t)x;
   }
 }
 
 template <int W, typename TKV, typename TQ>
-static cudaError_t launch_append_typed(const AppendParams &p, bool e4m3, cudaStream_t stream) {
-  if (!e4m3)
-    return launch_dependent(append_bf16_kernel<W, TKV, TQ>, dim3(p.b.num_rows),
-                            dim3(kAppendThreads), 0, stream, p);
-  const size_t smem = (size_t)kKvBlock * (8 * p.pairs + 4 * kAppendWarps * p.d);
-  cudaError_t e = cudaFuncSetAttribute(append_e4m3_kernel<W, TKV, TQ>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int units = p.b.q_start ? p.b.num_rows / kKvBlock + 2 * p.b.num_seqs : p.b.num_seqs;
-  return launch_dependent(append_e4m3_kernel<W, TKV, TQ>, dim3(units), dim3(kAppendThreads), smem,
-                          stream, p);
+static cudaError_t launch_append_typed(AppendParams p, bool e4m3, cudaStream_t stream) {
+  const int64_t units = p.b.q_start ? p.b.num_rows / kKvBlock + 2 * (int64_t)p.b.num_seqs : p.b.num_seqs;
+  // query heads of a thread block: 4 tasks a thread where units have 16 rows
+  const int rows = p.b.max_rows < kKvBlock ? p.b.max_rows : kKvBlock;
+  const int per = rotate_tasks<W>(p.d, p.pairs, p.interleaved);
+  int heads = 4 * kAppendThreads / (rows * per);
+  heads = heads < 1 ? 1 : heads > p.h_q ? p.h_q : heads;
+  p.q_heads = heads < 1 ? 1 : heads;
+  p.parts = 1 + (p.h_q + p.q_heads - 1) / p.q_heads;
+  if (units * p.parts > 2147483647) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)(units * p.parts)), block(kAppendThreads);
+  const size_t smem = sizeof(float2) * kKvBlock * p.pairs;
+  return e4m3 ? launch_dependent(append_kernel<W, TKV, TQ, true>, grid, block, smem, stream, p)
+              : launch_dependent(append_kernel<W, TKV, TQ, false>, grid, block, smem, stream, p);
 }
 
 template <int W>
@@ -332,7 +325,6 @@ cudaError_t launch_kv_append(const fathom_kv_append_args *a, const KvBatch &b, c
   p.b = b;
   p.d = a->cache.d;
   p.h_q = a->q ? a->h_q : 0;
-  p.G = 0;
   p.ck = a->cache.k;
   p.cv = a->cache.v;
   p.k_scale = a->cache.k_scale;
