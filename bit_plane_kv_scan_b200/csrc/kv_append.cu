@@ -2,18 +2,18 @@
 // rotated by their positions on the way.
 //
 // Row at position p, pair r: angle a = p f_r, (x, y) -> (x cos a - y sin a,
-// y cos a + x sin a).  The angle is formed and reduced to [-pi, pi] in fp64 (in
-// fp32 a position of a million turns by a wrong 0.06), then sincosf.
+// y cos a + x sin a).  The angle is formed and reduced to half a turn in fp64 (in
+// fp32 a position of a million turns by a wrong 0.06), then sincospif.
 //
 // A unit is the rows of one sequence that fall into one block of 16 positions.
-// Its first thread block takes keys and values, the others `q_heads` query heads
-// each; each works out the unit's sines and cosines for itself (1024 of them at
-// d = 128, against 32768 elements or more) and keeps them in shared memory.
+// A thread block works out its sines and cosines once (1024 of them at d = 128),
+// keeps them in shared memory and turns every head's rows; units of a few rows are
+// spread over several blocks.
 //
 // An E4M3 cache has a power-of-two scale per block of 16 tokens and KV head, so
 // a whole block belongs to one warp: it finds the largest new element, raises
 // the scale if it must, moves the codes that the block already held, and writes
-// the new ones (it reads its rows twice, the second time from L1).  The scale
+// the new ones.  The scale
 // comes from the elements before the rotation, which makes it the same whatever
 // the sines' last bit, and leaves room for sqrt 2.
 //
@@ -31,7 +31,9 @@ constexpr int kAppendThreads = 32 * kAppendWarps;
 struct AppendParams {
   KvBatch b;
   int d, h_q;          // (h_q: 0 without queries)
-  int q_heads, parts;  // query heads of a thread block, thread blocks of a unit
+  // a unit's work: q_parts of q_heads query heads each, then kv_parts of K and V; on
+  // one thread block (parts = 1) or on one for each part
+  int parts, q_parts, q_heads, kv_parts;
   void *ck, *cv;
   uint8_t *k_scale, *v_scale;
   const void *k, *v, *q;
@@ -64,74 +66,154 @@ struct alignas(N == 8 ? 16 : sizeof(T)) Vec {
   T x[N];
 };
 
-// cos and sin of p f, the angle in fp64.
+// cos and sin of p f.  The angle is formed in half turns, in fp64 with the
+// product's error carried along, and reduced to [-1, 1].
 __device__ __forceinline__ float2 cos_sin(int p, float f) {
-  const double a = (double)p * (double)f;
-  const double turns = rint(a * 0.15915494309189535);  // 1 / 2 pi
-  double r = fma(-turns, 6.283185307179586, a);
-  r = fma(-turns, 2.4492935982947064e-16, r);  // 2 pi less its fp64 value
+  constexpr double kInvPi = 0.31830988618379067;       // 1 / pi
+  constexpr double kInvPiLow = -1.9678676675182486e-17;  // 1 / pi less that
+  const double a = (double)p * (double)f;  // exact: 31 and 24 bits
+  const double h = a * kInvPi;
+  const double low = fma(a, kInvPi, -h) + a * kInvPiLow;
+  const double r = (h - 2.0 * rint(0.5 * h)) + low;
   float s, c;
-  sincosf((float)r, &s, &c);
+  sincospif((float)r, &s, &c);
   return make_float2(c, s);
 }
 
-// One row's head, rotated: task t of the head is elements of W pairs, or W
-// elements that stay.  `put(dim, Vec)` stores W elements from dimension dim.
-template <int W, typename T, typename Put>
-__device__ __forceinline__ void rotate_task(const T *head, int t, int d, int pairs, int interleaved,
-                                            const float2 *cs, Put put) {
-  const int turned = interleaved && W > 1 ? 2 * pairs / W : pairs / W;  // tasks with pairs
-  if (t >= turned) {
-    const int at = 2 * pairs + (t - turned) * W;
-    const Vec<T, W> v = *reinterpret_cast<const Vec<T, W> *>(head + at);
-    float o[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) o[i] = to_float(v.x[i]);
-    put(at, o, o);
+// A row's cosines and sines in shared memory: two neighbouring pairs of a task as
+// (cos, cos, sin, sin), the operands of two-wide arithmetic; the same two of
+// neighbouring tasks are neighbours, so that a warp's 16-byte reads hit different
+// banks.
+struct Turns {
+  int per;    // pairs of a task
+  int tasks;  // pairs / per
+  int row;    // float4s of a row
+  __host__ __device__ Turns(int w, int pairs, int interleaved) {
+    per = interleaved && w > 1 ? w / 2 : w;
+    tasks = pairs / per;
+    row = (per + 1) / 2 * tasks;
+  }
+  __device__ __forceinline__ void put(float4 *cs, int j, float2 c) const {
+    float *at = reinterpret_cast<float *>(cs + j % per / 2 * tasks + j / per) + (j % per & 1);
+    at[0] = c.x;
+    at[2] = c.y;
+  }
+};
+
+// Two fp32 operations in one.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(v));
+}
+
+// One row's head, rotated: task t of the head is W pairs (interleaved: W / 2), or
+// W elements that stay.
+template <int W, typename T>
+struct Task {
+  Vec<T, W> a, b;
+};
+
+__host__ __device__ __forceinline__ int turned_tasks(int W, int pairs, int interleaved) {
+  return interleaved && W > 1 ? 2 * pairs / W : pairs / W;
+}
+
+// FULL: every dimension is in a pair of halves (2 pairs = d, not interleaved), the
+// usual case, without the branches of the others.
+template <int W, bool FULL, typename T>
+__device__ __forceinline__ void load_task(Task<W, T> &x, const T *head, int t, int pairs,
+                                          int interleaved) {
+  auto at = [&](int i) { return *reinterpret_cast<const Vec<T, W> *>(head + i); };
+  if constexpr (FULL) {
+    x.a = at(t * W);
+    x.b = at(pairs + t * W);
     return;
   }
-  if (interleaved) {
-    if constexpr (W >= 2) {
-      const Vec<T, W> v = *reinterpret_cast<const Vec<T, W> *>(head + t * W);
-      float o[W], raw[W];
+  const int turned = turned_tasks(W, pairs, interleaved);
+  if (t >= turned) {
+    x.a = at(2 * pairs + (t - turned) * W);
+  } else if (interleaved) {
+    if constexpr (W > 1) {
+      x.a = at(t * W);
+    } else {
+      x.a = at(2 * t);
+      x.b = at(2 * t + 1);
+    }
+  } else {
+    x.a = at(t * W);
+    x.b = at(pairs + t * W);
+  }
+}
+
+// put(dim, W values) stores the task's elements from dimension dim.  Without cs
+// (then not interleaved) they stay as they are.
+template <int W, bool FULL, typename T, typename Put>
+__device__ __forceinline__ void rotate_task(const Task<W, T> &x, int t, int pairs, int interleaved,
+                                            const float4 *cs, Put put) {
+  const int turned = FULL ? pairs / W : turned_tasks(W, pairs, interleaved);
+  float oa[W], ob[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) oa[i] = to_float(x.a.x[i]);
+  if (!FULL && t >= turned) {
+    put(2 * pairs + (t - turned) * W, oa);
+    return;
+  }
+  if constexpr (W > 1 && !FULL) {
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const float4 c = cs[i / 4 * turned + t];
+        const float u = oa[i], v = oa[i + 1], y = oa[i + 2], z = oa[i + 3];
+        oa[i] = u * c.x - v * c.z;
+        oa[i + 1] = v * c.x + u * c.z;
+        oa[i + 2] = y * c.y - z * c.w;
+        oa[i + 3] = z * c.y + y * c.w;
+      }
+      put(t * W, oa);
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) ob[i] = to_float(x.b.x[i]);
+  if (cs) {
+    if constexpr (W > 1) {
 #pragma unroll
       for (int i = 0; i < W; i += 2) {
-        const float2 c = cs[(t * W + i) / 2];
-        const float x = to_float(v.x[i]), y = to_float(v.x[i + 1]);
-        raw[i] = x;
-        raw[i + 1] = y;
-        o[i] = x * c.x - y * c.y;
-        o[i + 1] = y * c.x + x * c.y;
+        const float4 c = cs[i / 2 * turned + t];
+        const uint64_t u = two(oa[i], oa[i + 1]), v = two(ob[i], ob[i + 1]), w = two(-ob[i], -ob[i + 1]);
+        const uint64_t cc = two(c.x, c.y), ss = two(c.z, c.w);
+        split2(fma2(w, ss, mul2(u, cc)), oa[i], oa[i + 1]);
+        split2(fma2(u, ss, mul2(v, cc)), ob[i], ob[i + 1]);
       }
-      put(t * W, o, raw);
     } else {
-      const float2 c = cs[t];
-      const float x[1] = {to_float(head[2 * t])}, y[1] = {to_float(head[2 * t + 1])};
-      const float ox[1] = {x[0] * c.x - y[0] * c.y}, oy[1] = {y[0] * c.x + x[0] * c.y};
-      put(2 * t, ox, x);
-      put(2 * t + 1, oy, y);
+      const float4 c = cs[t];
+      const float u = oa[0], v = ob[0];
+      oa[0] = u * c.x - v * c.z;
+      ob[0] = v * c.x + u * c.z;
     }
-    return;
   }
-  const Vec<T, W> a = *reinterpret_cast<const Vec<T, W> *>(head + t * W);
-  const Vec<T, W> b = *reinterpret_cast<const Vec<T, W> *>(head + pairs + t * W);
-  float oa[W], ob[W], ra[W], rb[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const float2 c = cs[t * W + i];
-    ra[i] = to_float(a.x[i]);
-    rb[i] = to_float(b.x[i]);
-    oa[i] = ra[i] * c.x - rb[i] * c.y;
-    ob[i] = rb[i] * c.x + ra[i] * c.y;
-  }
-  put(t * W, oa, ra);
-  put(pairs + t * W, ob, rb);
+  const bool beside = !FULL && W == 1 && interleaved;
+  put(beside ? 2 * t : t * W, oa);
+  put(beside ? 2 * t + 1 : pairs + t * W, ob);
 }
 
 // Tasks of one head: pairs W at a time, then the elements that stay.
 template <int W>
 __host__ __device__ __forceinline__ int rotate_tasks(int d, int pairs, int interleaved) {
-  return (interleaved && W > 1 ? 2 * pairs / W : pairs / W) + (d - 2 * pairs) / W;
+  return turned_tasks(W, pairs, interleaved) + (d - 2 * pairs) / W;
 }
 
 template <int W, typename T>
@@ -160,27 +242,48 @@ __device__ __forceinline__ float e4m3_float(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }
 
-// Rows m of a unit, `heads` heads each of `per` tasks, by the whole thread block:
-// fn(row, head, task).
-template <typename Fn>
-__device__ __forceinline__ void for_tasks(int m, int heads, int per, Fn fn) {
-  const int n = m * heads * per;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += kAppendThreads) {
-    const int t = i % per, rh = i / per;
-    fn(rh / heads, rh % heads, t);
+// The tasks of m rows, `heads` heads each of `per` tasks, dealt out to n threads of
+// which this is number i: load(task, row, head, t), then store(task, row, head, t).
+// The next task's loads are on their way while this one is worked on (the compiler
+// may not move a load over a store that could be to the same place), the first
+// one's while `meanwhile` runs.
+template <int W, typename T, typename Load, typename Store, typename Meanwhile>
+__device__ __forceinline__ void for_tasks(int i, int n, int m, int heads, int per, Load load,
+                                          Store store, Meanwhile meanwhile) {
+  int t = i % per, h = i / per % heads, r = i / per / heads;
+  const int dt = n % per, dh = n / per % heads, dr = n / per / heads;
+  Task<W, T> x;
+  if (r < m) load(x, r, h, t);
+  meanwhile();
+  while (r < m) {
+    int t2 = t + dt, h2 = h + dh, r2 = r + dr;
+    if (t2 >= per) {
+      t2 -= per;
+      ++h2;
+    }
+    if (h2 >= heads) {
+      h2 -= heads;
+      ++r2;
+    }
+    Task<W, T> y;
+    if (r2 < m) load(y, r2, h2, t2);
+    store(x, r, h, t);
+    x = y;
+    t = t2;
+    h = h2;
+    r = r2;
   }
 }
 
 // A sequence's m rows touch at most m / 16 + 2 blocks of positions, so the units
 // of sequence s start at q_start[s] / 16 + 2 s.
-template <int W, typename TKV, typename TQ, bool E4M3>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
+template <int W, typename TKV, typename TQ, bool E4M3, bool FULL>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
-  extern __shared__ float2 cs[];  // [16][pairs]
+  extern __shared__ float4 cs[];  // [16][Turns::row]
   const int d = p.d;
-  const int unit = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+  const int unit = blockIdx.x / p.parts, part0 = blockIdx.x % p.parts;
   int s = unit, u = 0;
   if (p.b.q_start) {
     auto base = [&](int i) { return (int64_t)(p.b.q_start[i] >> 4) + 2 * (int64_t)i; };
@@ -194,20 +297,34 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
   const int p0 = max(blk * kKvBlock, old), p1 = min((blk + 1) * kKvBlock, q.len);
   if (u < 0 || p1 <= p0) return;
   const int row0 = q.row0 + (p0 - old), m = p1 - p0;
-  for (int i = threadIdx.x; i < m * p.pairs; i += kAppendThreads)
-    cs[i] = cos_sin(p0 + i / p.pairs, p.inv_freq[i % p.pairs]);
-  __syncthreads();
+  const Turns lay(W, p.pairs, p.interleaved);
+  bool have = false;
+  auto turns = [&]() {  // the unit's cosines and sines, once
+    if (have) return;
+    have = true;
+    for (int i = threadIdx.x; i < m * p.pairs; i += kAppendThreads) {
+      const int r = i / p.pairs, j = i - r * p.pairs;
+      lay.put(cs + r * lay.row, j, cos_sin(p0 + r, p.inv_freq[j]));
+    }
+    __syncthreads();
+  };
+  auto nothing = []() {};
 
-  if (part > 0) {  // queries
-    const int h0 = (part - 1) * p.q_heads, heads = min(p.q_heads, p.h_q - h0);
+  for (int part = part0; part < p.q_parts; part += p.parts) {  // queries
+    const int h0 = part * p.q_heads, heads = min(p.q_heads, p.h_q - h0);
     const TQ *src = static_cast<const TQ *>(p.q) + (int64_t)row0 * p.q_stride + (int64_t)h0 * d;
     TQ *dst = static_cast<TQ *>(p.q_out) + ((int64_t)row0 * p.h_q + h0) * d;
-    for_tasks(m, heads, rotate_tasks<W>(d, p.pairs, p.interleaved), [&](int r, int h, int t) {
-      TQ *out = dst + ((int64_t)r * p.h_q + h) * d;
-      rotate_task<W>(src + r * p.q_stride + h * d, t, d, p.pairs, p.interleaved, cs + r * p.pairs,
-                     [&](int at, const float *o, const float *) { store_vec<W>(out + at, o); });
-    });
-    return;
+    for_tasks<W, TQ>(
+        threadIdx.x, kAppendThreads, m, heads, rotate_tasks<W>(d, p.pairs, p.interleaved),
+        [&](Task<W, TQ> &x, int r, int h, int t) {
+          load_task<W, FULL>(x, src + r * p.q_stride + h * d, t, p.pairs, p.interleaved);
+        },
+        [&](const Task<W, TQ> &x, int r, int h, int t) {
+          TQ *out = dst + ((int64_t)r * p.h_q + h) * d;
+          rotate_task<W, FULL>(x, t, p.pairs, p.interleaved, cs + r * lay.row,
+                         [&](int at, const float *o) { store_vec<W>(out + at, o); });
+        },
+        turns);
   }
   if (blk < 0) return;
   const int page = kv_page(p.b, s, blk * kKvBlock / p.b.page_tokens);
@@ -217,45 +334,121 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
   const int64_t head0 = (int64_t)page * p.b.h_kv;
   const TKV *k = static_cast<const TKV *>(p.k) + (int64_t)row0 * p.k_stride;
   const TKV *v = static_cast<const TKV *>(p.v) + (int64_t)row0 * p.v_stride;
-  const int per_k = rotate_tasks<W>(d, p.pairs, p.interleaved), per_v = d / W;
+  const int per_k = rotate_tasks<W>(d, p.pairs, p.interleaved);
 
+  const int kv0 = part0 < p.q_parts ? (p.parts == 1 ? 0 : p.kv_parts) : part0 - p.q_parts;
   if constexpr (!E4M3) {
+    if (kv0 >= p.kv_parts) return;
     auto place = [&](void *base, int r, int g) {
       return static_cast<__nv_bfloat16 *>(base) +
              ((head0 + g) * p.b.page_tokens + slot0 + held + r) * d;
     };
-    for_tasks(m, p.b.h_kv, per_k, [&](int r, int g, int t) {
-      __nv_bfloat16 *out = place(p.ck, r, g);
-      rotate_task<W>(k + r * p.k_stride + g * d, t, d, p.pairs, p.interleaved, cs + r * p.pairs,
-                     [&](int at, const float *o, const float *) { store_vec<W>(out + at, o); });
-    });
-    for_tasks(m, p.b.h_kv, per_v, [&](int r, int g, int t) {
-      rotate_task<W>(v + r * p.v_stride + g * d, t, d, 0, 0, cs,
-                     [&](int at, const float *o, const float *) { store_vec<W>(place(p.cv, r, g) + at, o); });
-    });
-    return;
+    for_tasks<W, TKV>(
+        threadIdx.x, kAppendThreads, m, p.b.h_kv, per_k,
+        [&](Task<W, TKV> &x, int r, int g, int t) {
+          load_task<W, FULL>(x, k + r * p.k_stride + g * d, t, p.pairs, p.interleaved);
+        },
+        [&](const Task<W, TKV> &x, int r, int g, int t) {
+          __nv_bfloat16 *out = place(p.ck, r, g);
+          rotate_task<W, FULL>(x, t, p.pairs, p.interleaved, cs + r * lay.row,
+                         [&](int at, const float *o) { store_vec<W>(out + at, o); });
+        },
+        turns);
+    for_tasks<W, TKV>(
+        threadIdx.x, kAppendThreads, m, p.b.h_kv, d / 2 / W,
+        [&](Task<W, TKV> &x, int r, int g, int t) {
+          load_task<W, true>(x, v + r * p.v_stride + g * d, t, d / 2, 0);
+        },
+        [&](const Task<W, TKV> &x, int r, int g, int t) {
+          __nv_bfloat16 *out = place(p.cv, r, g);
+          rotate_task<W, true>(x, t, d / 2, 0, nullptr,
+                               [&](int at, const float *o) { store_vec<W>(out + at, o); });
+        },
+        nothing);
   } else {
+    // a warp per KV head and side: keys first, so that most blocks of values need
+    // no turns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = warp; i < 2 * p.b.h_kv; i += kAppendWarps) {
+    for (int kv_part = kv0; kv_part < p.kv_parts; kv_part += p.parts) {
+      if (kv_part * kAppendWarps < p.b.h_kv) turns();
+      const int i = kv_part * kAppendWarps + warp;
+      if (i >= 2 * p.b.h_kv) break;
       const bool is_v = i >= p.b.h_kv;
       const int g = is_v ? i - p.b.h_kv : i;
-      const TKV *src = (is_v ? v : k) + g * d;
       const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      const TKV *src = (is_v ? v : k) + g * d;
       const int64_t head = head0 + g;
       uint8_t *scale = (is_v ? p.v_scale : p.k_scale) + head * (p.b.page_tokens / kKvBlock) +
                        slot0 / kKvBlock;
       uint8_t *codes = static_cast<uint8_t *>(is_v ? p.cv : p.ck) + (head * p.b.page_tokens + slot0) * d;
+      uint8_t *out = codes + held * d;
+      // values go in pairs of halves too, unturned
+      const int pairs = is_v ? d / 2 : p.pairs, inter = is_v ? 0 : p.interleaved;
+      const int per = rotate_tasks<W>(d, pairs, inter);
+      const int turned = FULL ? per : turned_tasks(W, pairs, inter);
+      const bool halves = FULL || W == 1 || !inter;  // a turned task has elements in both halves
       const int was = held ? kv_scale_exp(*scale) + 127 : 0;
       float big = 0.0f;
-#pragma unroll 4
-      for (int t = lane; t < m * per_v; t += 32) {
-        const int r = t / per_v;
-        const Vec<TKV, W> x = *reinterpret_cast<const Vec<TKV, W> *>(src + r * stride + (t - r * per_v) * W);
+      auto load = [&](Task<W, TKV> &x, int r, int, int t) {
+        load_task<W, FULL>(x, src + r * stride, t, pairs, inter);
+      };
+      // The largest finite element.  bf16: magnitudes are compared as 16-bit integers,
+      // two at a time; infinities and NaNs, which lie above, are rare enough to look
+      // for a second time.
+      uint32_t top = 0;
+      auto largest = [&](const Task<W, TKV> &x, int, int, int t) {
+        const bool both = FULL || (halves && t < turned);
+        if constexpr (W == 8 && sizeof(TKV) == 2) {
+          const uint4 a = *reinterpret_cast<const uint4 *>(&x.a), b = *reinterpret_cast<const uint4 *>(&x.b);
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+          if (both)
+#pragma unroll
+            for (int e = 4; e < 8; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+        } else {
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const float y = fabsf(to_float(x.a.x[e]));
+            if (y < INFINITY) big = fmaxf(big, y);
+            if (both) {
+              const float z = fabsf(to_float(x.b.x[e]));
+              if (z < INFINITY) big = fmaxf(big, z);
+            }
+          }
+        }
+      };
+      auto finite = [&](const Task<W, TKV> &x, int, int, int t) {
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          const float y = fabsf(to_float(x.x[e]));
+          const float y = fabsf(to_float(x.a.x[e]));
           if (y < INFINITY) big = fmaxf(big, y);
+          if (halves && t < turned) {
+            const float z = fabsf(to_float(x.b.x[e]));
+            if (z < INFINITY) big = fmaxf(big, z);
+          }
         }
+      };
+      // a block whose tasks fit into registers is read once
+      constexpr int kKeep = sizeof(TKV) == 2 ? 4 : 2;
+      Task<W, TKV> keep[kKeep];
+      const bool kept = m * per <= 32 * kKeep;
+      if (kept) {
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+          if (lane + 32 * j < m * per) load(keep[j], (lane + 32 * j) / per, 0, (lane + 32 * j) % per);
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+          if (lane + 32 * j < m * per) largest(keep[j], 0, 0, (lane + 32 * j) % per);
+      } else {
+        for_tasks<W, TKV>(lane, 32, m, 1, per, load, largest, nothing);
+      }
+      if constexpr (W == 8 && sizeof(TKV) == 2) {
+        top = max(top & 0xffffu, top >> 16);
+        if (__any_sync(0xffffffffu, top >= 0x7f80u))
+          for_tasks<W, TKV>(lane, 32, m, 1, per, load, finite, nothing);
+        else
+          big = __uint_as_float(top << 16);
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
@@ -272,21 +465,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
         x = was;
       }
       const float f = exp2i(127 - x);
-      uint8_t *out = codes + held * d;
-      const int per = is_v ? per_v : per_k, pairs = is_v ? 0 : p.pairs;
-#pragma unroll 4
-      for (int t = lane; t < m * per; t += 32) {
-        const int r = t / per;
-        rotate_task<W>(src + r * stride, t - r * per, d, pairs, is_v ? 0 : p.interleaved,
-                       cs + r * p.pairs, [&](int at, const float *o, const float *) {
-                         uint8_t *to = out + r * d + at;
-                         if constexpr (W == 8)
-                           *reinterpret_cast<uint2 *>(to) =
-                               make_uint2(pack_e4m3(o[0] * f, o[1] * f, o[2] * f, o[3] * f),
-                                          pack_e4m3(o[4] * f, o[5] * f, o[6] * f, o[7] * f));
-                         else
-                           *to = (uint8_t)__nv_cvt_float_to_fp8(o[0] * f, __NV_SATFINITE, __NV_E4M3);
-                       });
+      auto store = [&](const Task<W, TKV> &y, int r, int, int t) {
+        rotate_task<W, FULL>(y, t, pairs, inter, is_v ? nullptr : cs + r * lay.row, [&](int at, const float *o) {
+          uint8_t *to = out + r * d + at;
+          if constexpr (W == 8)
+            *reinterpret_cast<uint2 *>(to) = make_uint2(pack_e4m3(o[0] * f, o[1] * f, o[2] * f, o[3] * f),
+                                                        pack_e4m3(o[4] * f, o[5] * f, o[6] * f, o[7] * f));
+          else
+            *to = (uint8_t)__nv_cvt_float_to_fp8(o[0] * f, __NV_SATFINITE, __NV_E4M3);
+        });
+      };
+      if (kept) {
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+          if (lane + 32 * j < m * per) store(keep[j], (lane + 32 * j) / per, 0, (lane + 32 * j) % per);
+      } else {
+        for_tasks<W, TKV>(lane, 32, m, 1, per, load, store, nothing);
       }
       if (lane == 0) *scale = (uint8_t)x;
     }
@@ -296,18 +490,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) 
 template <int W, typename TKV, typename TQ>
 static cudaError_t launch_append_typed(AppendParams p, bool e4m3, cudaStream_t stream) {
   const int64_t units = p.b.q_start ? p.b.num_rows / kKvBlock + 2 * (int64_t)p.b.num_seqs : p.b.num_seqs;
-  // query heads of a thread block: 4 tasks a thread where units have 16 rows
+  // Units of 16 rows keep a thread block busy, which then works out their sines and
+  // cosines once; units of a row or a few are spread out, a task a thread.
   const int rows = p.b.max_rows < kKvBlock ? p.b.max_rows : kKvBlock;
+  const bool spread = rows < kKvBlock;
   const int per = rotate_tasks<W>(p.d, p.pairs, p.interleaved);
-  int heads = 4 * kAppendThreads / (rows * per);
-  heads = heads < 1 ? 1 : heads > p.h_q ? p.h_q : heads;
+  int heads = spread ? kAppendThreads / (rows * per) : p.h_q;
+  heads = heads > p.h_q ? p.h_q : heads;
   p.q_heads = heads < 1 ? 1 : heads;
-  p.parts = 1 + (p.h_q + p.q_heads - 1) / p.q_heads;
+  p.q_parts = (p.h_q + p.q_heads - 1) / p.q_heads;
+  p.kv_parts = e4m3 ? (2 * p.b.h_kv + kAppendWarps - 1) / kAppendWarps : 1;
+  p.parts = spread ? p.q_parts + p.kv_parts : 1;
   if (units * p.parts > 2147483647) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(units * p.parts)), block(kAppendThreads);
-  const size_t smem = sizeof(float2) * kKvBlock * p.pairs;
-  return e4m3 ? launch_dependent(append_kernel<W, TKV, TQ, true>, grid, block, smem, stream, p)
-              : launch_dependent(append_kernel<W, TKV, TQ, false>, grid, block, smem, stream, p);
+  const size_t smem = sizeof(float4) * kKvBlock * Turns(W, p.pairs, p.interleaved).row;
+  if (!p.interleaved && 2 * p.pairs == p.d)
+    return e4m3 ? launch_dependent(append_kernel<W, TKV, TQ, true, true>, grid, block, smem, stream, p)
+                : launch_dependent(append_kernel<W, TKV, TQ, false, true>, grid, block, smem, stream, p);
+  return e4m3 ? launch_dependent(append_kernel<W, TKV, TQ, true, false>, grid, block, smem, stream, p)
+              : launch_dependent(append_kernel<W, TKV, TQ, false, false>, grid, block, smem, stream, p);
 }
 
 template <int W>
