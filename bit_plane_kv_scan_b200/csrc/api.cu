@@ -734,6 +734,7 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   p.v_scale = a->cache.v_scale;
   p.q = a->q;
   p.q_wide = aligned(a->q, 16) && p.q_stride % (p.q_bf16 ? 8 : 4) == 0;
+  p.out_wide = aligned(a->out, 16);
   p.out = a->out;
   p.lse = a->lse;
   unsigned char *base = static_cast<unsigned char *>(ws);

@@ -540,6 +540,10 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, fl
   const KvSeq q = kv_seq(a.b, s);
   if (row < q.row0 || row >= q.row0 + q.rows) return;
   const int col = (row - q.row0) * a.G + h % a.G, c0 = col / a.cols * a.cols;
+  // (many rows: the unit's number in order of work; those before tail_from are whole)
+  if (a.tail_from > 0 &&
+      (a.col_tiles - 1 - col / a.cols) * a.pairs + s * a.b.h_kv + h / a.G < a.tail_from)
+    return;
   const int c1 = min(c0 + a.cols, q.rows * a.G), first = q.len - q.rows;
   const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
   const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
@@ -694,9 +698,19 @@ void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
   if (most < 1) most = 1;
   const int64_t base = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles;
   int64_t splits;
+  a.tail_from = 0;
   if (a.many_rows) {
-    // one block an SM, and at least 8 tiles a block
-    splits = 148 / ((int64_t)a.pairs * a.col_tiles);
+    // One block an SM.  Fewer units than SMs: each is divided.  More, of about equal
+    // length (a chunk over a long context, a window): those that would be left over
+    // for a last, partly filled wave are divided to fill it.  (Units of a prompt from
+    // its start grow with their rows; the short ones come last and fill the gaps.)
+    const int64_t units = (int64_t)a.pairs * a.col_tiles;
+    const bool even = windowed || (int64_t)a.b.max_len >= 4 * (int64_t)a.b.max_rows;
+    splits = 148 / units;
+    if (units > 148 && even && a.pairs == all_pairs && units % 148) {
+      a.tail_from = (int)(units - units % 148);
+      splits = 148 / (units % 148);
+    }
     if (splits > most / 8) splits = most / 8;
   } else {
     // Runs of at least 4 tiles a warp.  Where every sequence goes through about the

@@ -19,7 +19,7 @@ struct KvAttnParams {
   const void *q;
   int64_t q_stride;
   int q_bf16;  // and out's type
-  int q_wide;  // 16-byte loads of q's rows are aligned
+  int q_wide, out_wide;  // 16-byte accesses of q's and out's rows are aligned
   int h_q, G;
   float qscale;       // softmax scale * log2(e)
   int window, sinks;  // window: above max_len where there is none
@@ -31,9 +31,10 @@ struct KvAttnParams {
   int many_rows;  // the tcgen05 kernel
   int cols, tile;
   int col_tiles, tiles_per_split, splits;
-  // many_rows: the (sequence, KV head) pairs of one launch, and the rows of a K
-  // or V box; e4m3: tokens of a pair in the widened copy (0: there is none)
-  int pair0, pairs, box_rows, n_pad;
+  // many_rows: the (sequence, KV head) pairs of one launch; the units in order of
+  // work from which on they are divided (the others are not); the rows of a K or V
+  // box; e4m3: tokens of a pair in the widened copy (0: there is none)
+  int pair0, pairs, tail_from, box_rows, n_pad;
   const uint16_t *wide;  // [2][pairs][n_pad][d] bf16
   WsStatus *status;
   int *taint;       // many_rows: [units][splits], see kv_prompt.cu

@@ -202,18 +202,29 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-// The units' order of work: later rows see more keys, so they come first.
+// The units' order of work: later rows see more keys, so they come first.  Units
+// from number tail_from on are divided over `splits` blocks each.
 struct Unit {
-  int split, pair, rb;
+  int split, splits, pair, rb;
 };
 
 __device__ __forceinline__ Unit unit_of(const KvAttnParams &a, int x) {
   Unit u;
-  u.split = x % a.splits;
-  x /= a.splits;
+  u.split = 0;
+  u.splits = 1;
+  if (x >= a.tail_from) {
+    u.split = (x - a.tail_from) % a.splits;
+    u.splits = a.splits;
+    x = a.tail_from + (x - a.tail_from) / a.splits;
+  }
   u.pair = a.pair0 + x % a.pairs;
   u.rb = a.col_tiles - 1 - x / a.pairs;
   return u;
+}
+
+__host__ __device__ __forceinline__ int unit_blocks(const KvAttnParams &a) {
+  const int units = a.pairs * a.col_tiles, tail = units > a.tail_from ? units - a.tail_from : 0;
+  return units - tail + tail * a.splits;
 }
 
 template <int D>
@@ -228,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_fault;
   grid_dependency_wait();
   allow_dependent_launch();
-  if ((int)blockIdx.x == a.pairs * a.col_tiles * a.splits) {  // one more, in the first launch
+  if ((int)blockIdx.x == unit_blocks(a)) {  // one more, in the first launch
     write_status(a);
     return;
   }
@@ -237,17 +248,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = u.split, rb = u.rb;
   const int head = u.pair % a.b.h_kv, s = u.pair / a.b.h_kv;
   int *taint = a.taint + ((int64_t)u.pair * a.col_tiles + rb) * a.splits + split;
-  if (tid == 0) *taint = 0;
+  if (tid < (u.splits == 1 ? a.splits : 1)) taint[tid] = 0;
   const KvSeq q = kv_seq(a.b, s);
   const int c0 = rb * kPromptCols, c1 = min(c0 + kPromptCols, q.rows * a.G);
   if (c0 >= c1) return;
   const int first = q.len - q.rows;  // position of the sequence's first row
   const int p_lo = first + c0 / a.G, p_hi = first + (c1 - 1) / a.G;
   const KvTiles tiles = visible_tiles(a, p_lo, p_hi, kN);
-  const int i0 = split * a.tiles_per_split;
-  const int nt = min(tiles.count - i0, a.tiles_per_split);  // tiles of this block
+  const int run = u.splits == 1 ? tiles.count : a.tiles_per_split;
+  const int i0 = split * run;
+  const int nt = min(tiles.count - i0, run);  // tiles of this block
   if (split > 0 && nt <= 0) return;
   const int n_m = c1 - c0 > kM ? 2 : 1;  // tiles of rows
+
+  // The softmax warps' 32 rows of Q each (zeros behind the last; its sign makes the
+  // scale positive), a row by 16 or 8 lanes: on their way while the block sets up.
+  uint4 xq[D / 8];
+  if (warp < kSoftWarps && nt > 0) {
+    const uint32_t flip = a.qscale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const int c = c0 + 32 * warp + (32 * i + lane) / (D / 8);
+      xq[i] = make_uint4(0, 0, 0, 0);
+      if (c < c1) {
+        const uint16_t *e = static_cast<const uint16_t *>(a.q) + (int64_t)(q.row0 + c / a.G) * a.q_stride +
+                            (int64_t)(head * a.G + c % a.G) * D + 8 * (lane % (D / 8));
+        if (a.q_wide) {
+          xq[i] = __ldg(reinterpret_cast<const uint4 *>(e));
+        } else {
+          xq[i].x = e[0] | ((uint32_t)e[1] << 16);
+          xq[i].y = e[2] | ((uint32_t)e[3] << 16);
+          xq[i].z = e[4] | ((uint32_t)e[5] << 16);
+          xq[i].w = e[6] | ((uint32_t)e[7] << 16);
+        }
+        xq[i].x ^= flip;
+        xq[i].y ^= flip;
+        xq[i].z ^= flip;
+        xq[i].w ^= flip;
+      }
+    }
+  }
 
   const uint32_t base = (tc_smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sq = base, ring = base + 2 * kTile;
@@ -310,34 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float ref = -INFINITY, l = 0.0f;
     bool live = true;
     if (nt > 0 && m < n_m) {
-      {  // this thread's row of Q (zeros behind the last); its sign makes cs >= 0
-        const uint32_t flip = a.qscale < 0.0f ? 0x80008000u : 0u;
-        const uint16_t *src = static_cast<const uint16_t *>(a.q) +
-                              (int64_t)(q.row0 + c / a.G) * a.q_stride +
-                              (int64_t)(head * a.G + c % a.G) * D;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (c < c1) {
-            const uint16_t *e = src + 8 * i;
-            if (a.q_wide) {
-              x = *reinterpret_cast<const uint4 *>(e);
-            } else {
-              x.x = e[0] | ((uint32_t)e[1] << 16);
-              x.y = e[2] | ((uint32_t)e[3] << 16);
-              x.z = e[4] | ((uint32_t)e[5] << 16);
-              x.w = e[6] | ((uint32_t)e[7] << 16);
-            }
-            x.x ^= flip;
-            x.y ^= flip;
-            x.z ^= flip;
-            x.w ^= flip;
-          }
-          st_shared16(sq + m * kTile + (i / 8) * kPanel + r * 128 + (((i % 8) ^ (r & 7)) << 4), x);
-        }
-        proxy_fence();
-        mbar_arrive(q_full(m));
+      for (int i = 0; i < D / 8; ++i) {
+        const int rr = 32 * (warp & 3) + (32 * i + lane) / (D / 8), ch = lane % (D / 8);
+        st_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 + (((ch % 8) ^ (rr & 7)) << 4), xq[i]);
       }
+      proxy_fence();
+      mbar_arrive(q_full(m));
       const int t_lo = first + (c0 + m * kM) / a.G;
       const int t_hi = first + (min(c0 + m * kM + kM, c1) - 1) / a.G;
       // blocks of 16 keys that are there, of tile j
@@ -452,16 +471,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_ld32(t_o(m) + lanes + 32 * i, v);
           tc_wait_ld();
         }
-        if (!mine) continue;
-        if (a.splits == 1) {
-          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + rh * D + 32 * i;
+        if (u.splits == 1) {
+          // by way of the tile's rows of Q, which no product reads any more: a row's
+          // 64 bytes here, whole rows to the output below
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float x0 = l == 0.0f ? 0.0f : __uint_as_float(v[e]) * inv;
-            const float x1 = l == 0.0f ? 0.0f : __uint_as_float(v[e + 1]) * inv;
-            reinterpret_cast<__nv_bfloat162 *>(out)[e / 2] = __floats2bfloat162_rn(x0, x1);
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              w[z] = bf16x2(l == 0.0f ? 0.0f : __uint_as_float(v[e + 2 * z]) * inv,
+                            l == 0.0f ? 0.0f : __uint_as_float(v[e + 2 * z + 1]) * inv);
+            const int ch = 4 * i + e / 8;
+            st_shared16(sq + m * kTile + (ch / 8) * kPanel + r * 128 + (((ch % 8) ^ (r & 7)) << 4),
+                        make_uint4(w[0], w[1], w[2], w[3]));
           }
-        } else {
+        } else if (mine) {
           float *out = a.part_o + part * D + 32 * i;
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
@@ -471,8 +495,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
         }
       }
+      if (u.splits == 1) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const int rr = 32 * (warp & 3) + (32 * i + lane) / (D / 8), ch = lane % (D / 8);
+          const int cc = c0 + m * kM + rr;
+          if (cc < c1) {
+            const uint4 x = ld_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 +
+                                        (((ch % 8) ^ (rr & 7)) << 4));
+            const int64_t at = (int64_t)(q.row0 + cc / a.G) * a.h_q + head * a.G + cc % a.G;
+            if (a.out_wide) {
+              *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + 8 * ch) = x;
+            } else {
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int z = 0; z < 8; ++z)
+                static_cast<uint16_t *>(a.out)[at * D + 8 * ch + z] = (uint16_t)(w[z / 2] >> (16 * (z & 1)));
+            }
+          }
+        }
+      }
       if (mine) {
-        if (a.splits == 1) {
+        if (u.splits == 1) {
           if (a.lse) a.lse[rh] = lse_of(ref, l, 0.0f);
         } else {
           a.part_ml[part] = make_float2(ref, l);
@@ -529,9 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = 2 * j + 1, st = x % kStages;
         const int key0 = kN * tiles.at(i0 + j);
         // a tile that every row sees whole needs nothing, if its pages are there
-        const bool gone = page_of(key0 + kKvBlock * (lane & 7)) < 0;
-        const bool edge =
-            __any_sync(0xffffffffu, gone) || !sees_all(a, p_lo, p_hi, key0, kN);
+        const uint32_t there =
+            __ballot_sync(0xffffffffu, page_of(key0 + kKvBlock * (lane & 7)) >= 0);
+        const bool edge = (there & 0xffu) != 0xffu || !sees_all(a, p_lo, p_hi, key0, kN);
         if (!warp_wait(kv_full(st), (x / kStages) & 1)) {
           s_fault = 1;
           break;
@@ -539,11 +584,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) {
           uint32_t bad = 0;
           for (int r = t; r < kN; r += kEdgeThreads) {
+            const int key = key0 + r;
+            const bool seen = seen_by_some(key) && (there >> (r / kKvBlock) & 1);
+            if (seen && sees_all(a, p_lo, p_hi, key, 1)) continue;
             const uint32_t at = ring + st * kTile + r * 128;
-            const bool seen = seen_by_some(key0 + r) && page_of(key0 + r) >= 0;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              const uint32_t w = at + (i / 8) * kPanel + 16 * (i % 8);
+            for (int i = 0; i < D / 8; ++i) {  // (each lane starts elsewhere: other banks)
+              const uint32_t w = at + (i / 8) * kPanel + 16 * ((i + lane) % 8);
               if (!seen) {
                 st_shared16(w, make_uint4(0, 0, 0, 0));
               } else {
@@ -727,7 +774,7 @@ cudaError_t launch(KvAttnParams a, bool f8, cudaStream_t s) {
                            static_cast<uint16_t *>(const_cast<void *>(v)));
     if (e == cudaSuccess)
       e = launch_dependent(kv_prompt_kernel<D>,
-                           dim3((unsigned)(a.pairs * a.col_tiles * a.splits + (a.pair0 == 0))),
+                           dim3((unsigned)(unit_blocks(a) + (a.pair0 == 0))),
                            dim3(kThreads), smem, s, a, map_k, map_v);
   }
   return e;
