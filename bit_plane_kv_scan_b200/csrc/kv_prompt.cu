@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTile = tile_bytes<D>();
   constexpr int kSteps = D / 16;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[3 * kStages + 2 + 4 + 1];
+  __shared__ __align__(8) uint64_t s_bar[3 * kStages + 2 + 2 + 4 + 1];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fault;
   grid_dependency_wait();
@@ -297,8 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v_ready = [&](int i) { return bar0 + 8 * (2 * kStages + i); };  // V's edges are in order
   auto q_full = [&](int i) { return bar0 + 8 * (3 * kStages + i); };
   auto s_full = [&](int i) { return bar0 + 8 * (3 * kStages + 2 + i); };
-  auto p_full = [&](int i) { return bar0 + 8 * (3 * kStages + 4 + i); };
-  const uint32_t o_full = bar0 + 8 * (3 * kStages + 6);
+  // half of P_i: its keys 0-63, 64-127
+  auto p_full = [&](int i, int half) { return bar0 + 8 * (3 * kStages + 4 + 2 * i + half); };
+  const uint32_t o_full = bar0 + 8 * (3 * kStages + 8);
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
@@ -316,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full(i), kM);
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), kM);
+      mbar_init(p_full(i, 0), kM);
+      mbar_init(p_full(i, 1), kM);
     }
     mbar_init(o_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -444,12 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[e / 2] = bf16x2(p0, p1);
           }
           tc_st16(t_s(m) + lanes + 16 * i, w);
+          if (i % 2) {  // half of the row: its product can start
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full(m, i / 2));
+          }
         }
         const float2 part = unpack2(add2(sum, sum2));
         l += part.x + part.y;
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(p_full(m));
       }
       if (live) live = warp_wait(o_full, 0);
       if (!live) s_fault = 1;
@@ -623,10 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                  kIdS, k > 0);
         }
       };
-      auto mul_o = [&](int m, int stage, bool acc) {
+      auto mul_o = [&](int m, int half, int stage, bool acc) {
         if (!leader) return;
 #pragma unroll
-        for (int k = 0; k < kN / 16; ++k)
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
           mma_ts(t_o(m), t_s(m) + 8 * k, smem_desc(ring + stage * kTile + k * 2048, kPanel), kIdO,
                  acc || k > 0);
       };
@@ -647,9 +651,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(v_ready(xv % kStages), (j >> 1) & 1)) break;
         if (more && !wait(kv_full(xk % kStages), (xk / kStages) & 1)) break;
         for (int m = 0; m < n_m; ++m) {
-          if (!wait(p_full(m), j & 1)) break;
+          if (!wait(p_full(m, 0), j & 1)) break;
           tc_fence_after();
-          mul_o(m, xv % kStages, j > 0);
+          mul_o(m, 0, xv % kStages, j > 0);
+          if (!wait(p_full(m, 1), j & 1)) break;
+          tc_fence_after();
+          mul_o(m, 1, xv % kStages, true);
           if (m == n_m - 1) commit(kv_empty(xv % kStages));
           if (more) {
             mul_s(m, xk % kStages);
