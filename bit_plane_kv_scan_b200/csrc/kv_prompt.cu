@@ -361,16 +361,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(q_full(m));
       const int t_lo = first + (c0 + m * kM) / a.G;
       const int t_hi = first + (min(c0 + m * kM + kM, c1) - 1) / a.G;
-      // blocks of 16 keys that are there, of tile j
-      auto blocks_of = [&](int j) {
+      // lane b: the page table's entry for block b of 16 keys of tile j.  It is looked at
+      // a tile later, so that nothing waits for it.
+      auto entry_of = [&](int j) {
         const int key = kN * tiles.at(i0 + j) + kKvBlock * (lane & 7);
-        return __ballot_sync(0xffffffffu, page_of(key) >= 0) & 0xffu;
+        const int at = (int)((unsigned)key / (unsigned)a.b.page_tokens);
+        return key < q.len && at < a.b.table_width
+                   ? __ldg(a.b.page_table + (int64_t)s * a.b.table_width + at)
+                   : -1;
       };
-      uint32_t blocks = blocks_of(0);
+      int entry = entry_of(0);
       for (int j = 0; j < nt; ++j) {
         const int key0 = kN * tiles.at(i0 + j);
-        const uint32_t here = blocks;
-        if (j + 1 < nt) blocks = blocks_of(j + 1);
+        const uint32_t here =
+            __ballot_sync(0xffffffffu, entry >= 0 && entry < a.b.num_pages) & 0xffu;
+        if (j + 1 < nt) entry = entry_of(j + 1);
         const bool whole = here == 0xffu && sees_all(a, t_lo, t_hi, key0, kN);
         // the keys that this row sees, of 32 from key0 + 32 i
         auto seen = [&](int i) {
