@@ -261,30 +261,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (split > 0 && nt <= 0) return;
   const int n_m = c1 - c0 > kM ? 2 : 1;  // tiles of rows
 
-  // The softmax warps' 32 rows of Q each (zeros behind the last; its sign makes the
-  // scale positive), a row by 16 or 8 lanes: on their way while the block sets up.
+  // The softmax warps' 32 rows of Q each (zeros behind the last), a row by 16 or 8
+  // lanes: all on their way while the block sets up, looked at afterwards.
   uint4 xq[D / 8];
   if (warp < kSoftWarps && nt > 0) {
-    const uint32_t flip = a.qscale < 0.0f ? 0x80008000u : 0u;
+    const uint16_t *rows = static_cast<const uint16_t *>(a.q) + 8 * (lane % (D / 8));
+    auto row_of = [&](int i) {  // a row behind the last: the last
+      const int c = min(c0 + 32 * warp + (32 * i + lane) / (D / 8), c1 - 1);
+      return rows + (int64_t)(q.row0 + c / a.G) * a.q_stride + (int64_t)(head * a.G + c % a.G) * D;
+    };
+    if (a.q_wide) {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const int c = c0 + 32 * warp + (32 * i + lane) / (D / 8);
-      xq[i] = make_uint4(0, 0, 0, 0);
-      if (c < c1) {
-        const uint16_t *e = static_cast<const uint16_t *>(a.q) + (int64_t)(q.row0 + c / a.G) * a.q_stride +
-                            (int64_t)(head * a.G + c % a.G) * D + 8 * (lane % (D / 8));
-        if (a.q_wide) {
-          xq[i] = __ldg(reinterpret_cast<const uint4 *>(e));
-        } else {
-          xq[i].x = e[0] | ((uint32_t)e[1] << 16);
-          xq[i].y = e[2] | ((uint32_t)e[3] << 16);
-          xq[i].z = e[4] | ((uint32_t)e[5] << 16);
-          xq[i].w = e[6] | ((uint32_t)e[7] << 16);
-        }
-        xq[i].x ^= flip;
-        xq[i].y ^= flip;
-        xq[i].z ^= flip;
-        xq[i].w ^= flip;
+      for (int i = 0; i < D / 8; ++i) xq[i] = __ldg(reinterpret_cast<const uint4 *>(row_of(i)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint16_t *e = row_of(i);
+        xq[i] = make_uint4(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16),
+                           e[4] | ((uint32_t)e[5] << 16), e[6] | ((uint32_t)e[7] << 16));
       }
     }
   }
@@ -352,10 +346,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     float ref = -INFINITY, l = 0.0f;
     bool live = true;
     if (nt > 0 && m < n_m) {
+      const uint32_t flip = a.qscale < 0.0f ? 0x80008000u : 0u;  // makes the scale positive
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const int rr = 32 * (warp & 3) + (32 * i + lane) / (D / 8), ch = lane % (D / 8);
-        st_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 + (((ch % 8) ^ (rr & 7)) << 4), xq[i]);
+        uint4 x = xq[i];
+        x.x ^= flip;
+        x.y ^= flip;
+        x.z ^= flip;
+        x.w ^= flip;
+        if (c0 + m * kM + rr >= c1) x = make_uint4(0, 0, 0, 0);
+        st_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 + (((ch % 8) ^ (rr & 7)) << 4), x);
       }
       proxy_fence();
       mbar_arrive(q_full(m));
