@@ -4,11 +4,15 @@
 // A unit is 256 (token, head) pairs of one sequence and KV head, as two tiles
 // of 128 rows: the G heads that share a KV head share its keys.  One
 // thread block per SM takes a unit through its keys, 128 at a time:
-//   S_i = Q_i K^T      tcgen05.mma, Q and K in shared memory, S_i in tensor memory
-//   P_i = 2^(c S_i - m_i)   one thread a row, rounded to bf16, over S_i's columns
+//   S = Q_i K^T        tcgen05.mma, Q and K in shared memory, S in tensor memory
+//   P_i = 2^(c S - m_i)     one thread a row, from registers, rounded to bf16
 //   O_i += P_i V       tcgen05.mma, P_i from tensor memory, O_i stays there
 // with c = scale * log2 e.  The two tiles alternate, so that the tensor cores
-// multiply one while the other's softmax is worked out.  A row's reference m
+// multiply one while the other's softmax is worked out.  The softmax takes a whole
+// row of S into registers at once, so one S serves both tiles and the next scores
+// are ready when a softmax ends.  (With an S for each tile, P over its columns, a
+// tile's next scores had to wait for its softmax and its product with V: 3700
+// clocks for a tile of keys, of which 2600 were softmax.)  A row's reference m
 // moves only when its maximum has grown by more than 2^8 (weights up to 2^8 are as
 // exact in bf16 and fp32 as those up to 1); then the row of O is rescaled.
 //
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTile = tile_bytes<D>();
   constexpr int kSteps = D / 16;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[3 * kStages + 2 + 2 + 4 + 1];
+  __shared__ __align__(8) uint64_t s_bar[3 * kStages + 12];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fault;
   grid_dependency_wait();
@@ -293,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_full = [&](int i) { return bar0 + 8 * (3 * kStages + 2 + i); };
   // half of P_i: its keys 0-63, 64-127
   auto p_full = [&](int i, int half) { return bar0 + 8 * (3 * kStages + 4 + 2 * i + half); };
-  const uint32_t o_full = bar0 + 8 * (3 * kStages + 8);
+  auto s_read = [&](int i) { return bar0 + 8 * (3 * kStages + 8 + i); };   // S is in registers
+  auto o_done = [&](int i) { return bar0 + 8 * (3 * kStages + 10 + i); };  // O_i += P_i V
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
@@ -313,8 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i, 0), kM);
       mbar_init(p_full(i, 1), kM);
+      mbar_init(s_read(i), kM);
+      mbar_init(o_done(i), 1);
     }
-    mbar_init(o_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     s_fault = 0;
   }
@@ -322,8 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // tensor memory: S_0, S_1 (P_i over their first half), O_0, O_1
-  auto t_s = [&](int i) { return tmem + kN * i; };
+  // tensor memory: S (of one tile at a time), P_0, P_1, O_0, O_1
+  const uint32_t t_s = tmem;
+  auto t_p = [&](int i) { return tmem + kN + kN / 2 * i; };
   auto t_o = [&](int i) { return tmem + 2 * kN + D * i; };
   // the page of the token `key`, -1 where there is none
   auto page_of = [&](int key) {
@@ -394,8 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t v[kN / 32][32];
 #pragma unroll
-        for (int i = 0; i < kN / 32; ++i) tc_ld32(t_s(m) + lanes + 32 * i, v[i]);
+        for (int i = 0; i < kN / 32; ++i) tc_ld32(t_s + lanes + 32 * i, v[i]);
         tc_wait_ld();
+        tc_fence_before();
+        mbar_arrive(s_read(m));
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < kN / 32; ++i) {
@@ -416,6 +425,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         mx = mx == -INFINITY ? mx : mx * cs;
+        // the product with the tile before is complete: O and P may change
+        if (j > 0 && !warp_wait(o_done(m), (j - 1) & 1)) {
+          live = false;
+          break;
+        }
+        tc_fence_after();
         const bool grow = mx > ref + kSlack;
         if (__any_sync(0xffffffffu, grow)) {
           const float next = grow ? mx : ref;
@@ -451,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum = add2(sum, pack2(p0, p1));
             w[e / 2] = bf16x2(p0, p1);
           }
-          tc_st16(t_s(m) + lanes + 16 * i, w);
+          tc_st16(t_p(m) + lanes + 16 * i, w);
           if (i % 2) {  // half of the row: its product can start
             tc_wait_st();
             tc_fence_before();
@@ -461,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 part = unpack2(add2(sum, sum2));
         l += part.x + part.y;
       }
-      if (live) live = warp_wait(o_full, 0);
+      if (live) live = warp_wait(o_done(m), (nt - 1) & 1);
       if (!live) s_fault = 1;
       tc_fence_after();
     }
@@ -629,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
-          mma_ss(t_s(m), smem_desc(sq + m * kTile + off, 16), smem_desc(ring + stage * kTile + off, 16),
+          mma_ss(t_s, smem_desc(sq + m * kTile + off, 16), smem_desc(ring + stage * kTile + off, 16),
                  kIdS, k > 0);
         }
       };
@@ -637,51 +652,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!leader) return;
 #pragma unroll
         for (int k = 4 * half; k < 4 * half + 4; ++k)
-          mma_ts(t_o(m), t_s(m) + 8 * k, smem_desc(ring + stage * kTile + k * 2048, kPanel), kIdO,
+          mma_ts(t_o(m), t_p(m) + 8 * k, smem_desc(ring + stage * kTile + k * 2048, kPanel), kIdO,
                  acc || k > 0);
       };
       auto commit = [&](uint32_t bar) {
         if (leader) tc_commit(bar);
       };
+      // P_m V of tile j, half by half
+      auto add_o = [&](int m, int j) {
+        const int st = (2 * j + 1) % kStages;
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(p_full(m, half), j & 1)) return;
+          tc_fence_after();
+          mul_o(m, half, st, j > 0 || half > 0);
+        }
+        commit(o_done(m));
+      };
+      // The next tile's S_0 comes before this one's P_0 V, so that a row tile's next
+      // scores wait for its softmax and not the other way round.  There is room for
+      // one S: each is multiplied once the softmax has read the one before.
       if (wait(kv_full(0), 0)) {
         tc_fence_after();
-        for (int m = 0; m < n_m; ++m) {
-          mul_s(m, 0);
-          commit(s_full(m));
+        mul_s(0, 0);
+        commit(s_full(0));
+        if (n_m == 2 && wait(s_read(0), 0)) {
+          tc_fence_after();
+          mul_s(1, 0);
+          commit(s_full(1));
         }
         commit(kv_empty(0));
       }
       for (int j = 0; j < nt && live; ++j) {
-        const int xv = 2 * j + 1, xk = 2 * j + 2;  // ring items: V of this tile, K of the next
+        const int st = (2 * j + 2) % kStages;  // K of the next tile
         const bool more = j + 1 < nt;
-        if (!wait(v_ready(xv % kStages), (j >> 1) & 1)) break;
-        if (more && !wait(kv_full(xk % kStages), (xk / kStages) & 1)) break;
-        for (int m = 0; m < n_m; ++m) {
-          if (!wait(p_full(m, 0), j & 1)) break;
+        if (more) {
+          if (!wait(kv_full(st), ((2 * j + 2) / kStages) & 1)) break;
+          if (!wait(s_read(n_m - 1), j & 1)) break;
           tc_fence_after();
-          mul_o(m, 0, xv % kStages, j > 0);
-          if (!wait(p_full(m, 1), j & 1)) break;
-          tc_fence_after();
-          mul_o(m, 1, xv % kStages, true);
-          if (m == n_m - 1) commit(kv_empty(xv % kStages));
-          if (more) {
-            mul_s(m, xk % kStages);
-            commit(s_full(m));
-          }
+          mul_s(0, st);
+          commit(s_full(0));
+          if (n_m == 1) commit(kv_empty(st));
         }
-        if (more) commit(kv_empty(xk % kStages));
+        if (!wait(v_ready((2 * j + 1) % kStages), (j >> 1) & 1)) break;
+        add_o(0, j);
+        if (n_m == 2) {
+          if (more) {
+            if (!wait(s_read(0), (j + 1) & 1)) break;
+            tc_fence_after();
+            mul_s(1, st);
+            commit(s_full(1));
+            commit(kv_empty(st));
+          }
+          add_o(1, j);
+        }
+        commit(kv_empty((2 * j + 1) % kStages));
       }
-      commit(o_full);
       if (!live) s_fault = 1;
     }
   }
 
-  // Every MMA is complete once o_full has arrived; then the ring's last commits
-  // are waited for, so that no arrival is pending when the barriers go away.
+  // The ring's last commits are waited for: then every MMA is complete, and no
+  // arrival is pending when the barriers go away.
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && nt > 0) {
-    if (!mbar_wait(o_full, 0)) s_fault = 1;
     for (int i = 0; i < kStages && !s_fault; ++i) {
       const int items = (2 * nt - i + kStages - 1) / kStages;
       if (items > 0 && !mbar_wait(kv_empty(i), (items - 1) & 1)) s_fault = 1;
@@ -690,6 +724,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (tid == 0 && s_fault) atomicAdd(&a.status->device_faults, 1u);
   tc_fence_after();
+  if (warp == kMmaWarp && s_fault) {  // given up halfway: what was issued ends first
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1ll << 24)) {
+    }
+  }
+  __syncwarp();
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem),
                  "r"(kTmemCols)
