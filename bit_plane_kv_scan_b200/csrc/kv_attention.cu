@@ -667,7 +667,7 @@ void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
   // counts the cache's rows in 31 bits.)
   const int64_t rows = (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
   a.many_rows = a.q_bf16 && (d == 64 || d == 128) && (int64_t)a.b.max_rows * a.G >= 64 &&
-                (f8 || rows < ((int64_t)1 << 31));
+                a.G <= 4096 && (f8 || rows < ((int64_t)1 << 31));
   const int64_t all_pairs = (int64_t)a.b.num_seqs * a.b.h_kv;
   a.pair0 = 0;
   a.pairs = (int)all_pairs;

@@ -206,6 +206,23 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
+// Columns c0 + x of a unit (x < 65536 - G) as rows and heads, without a division each.
+struct Columns {
+  int row, head, G;
+  uint32_t magic;  // 2^32 / G, rounded up
+  __device__ __forceinline__ Columns(int c0, int heads) {
+    G = heads;
+    row = c0 / heads;
+    head = c0 - row * heads;
+    magic = 0xffffffffu / (uint32_t)heads + 1;  // (0 for G = 1)
+  }
+  // row (past c0's) and head of column c0 + x; exact while x + head < 2^16, G < 2^16
+  __device__ __forceinline__ int row_of(int x) const {
+    return G == 1 ? x : (int)__umulhi((uint32_t)(head + x), magic);
+  }
+  __device__ __forceinline__ int head_of(int x) const { return head + x - row_of(x) * G; }
+};
+
 // The units' order of work: later rows see more keys, so they come first.  Units
 // from number tail_from on are divided over `splits` blocks each.
 struct Unit {
@@ -264,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nt = min(tiles.count - i0, run);  // tiles of this block
   if (split > 0 && nt <= 0) return;
   const int n_m = c1 - c0 > kM ? 2 : 1;  // tiles of rows
+  const Columns cols(c0, a.G);
 
   // The softmax warps' 32 rows of Q each (zeros behind the last), a row by 16 or 8
   // lanes: all on their way while the block sets up, looked at afterwards.
@@ -271,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kSoftWarps && nt > 0) {
     const uint16_t *rows = static_cast<const uint16_t *>(a.q) + 8 * (lane % (D / 8));
     auto row_of = [&](int i) {  // a row behind the last: the last
-      const int c = min(c0 + 32 * warp + (32 * i + lane) / (D / 8), c1 - 1);
-      return rows + (int64_t)(q.row0 + c / a.G) * a.q_stride + (int64_t)(head * a.G + c % a.G) * D;
+      const int x = min(32 * warp + (32 * i + lane) / (D / 8), c1 - 1 - c0);
+      return rows + (int64_t)(q.row0 + cols.row + cols.row_of(x)) * a.q_stride +
+             (head * a.G + cols.head_of(x)) * D;
     };
     if (a.q_wide) {
 #pragma unroll
@@ -307,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
-  if (tid == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(kv_full(i), 1);
       mbar_init(kv_empty(i), 1);
@@ -324,6 +343,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     s_fault = 0;
   }
+  // the page of the token `key`, -1 where there is none
+  auto page_of = [&](int key) {
+    return key < q.len ? kv_page(a.b, s, (int)((unsigned)key / (unsigned)a.b.page_tokens)) : -1;
+  };
+  // K and V of tile j into the ring, by the TMA warp: a lane per box (box_rows rows of
+  // one page, 64 dimensions).  False if the ring's places did not become free.
+  constexpr int kPanels = D / 64;
+  const int box_row = lane / kPanels * a.box_rows, box_panel = lane % kPanels;
+  auto place = [&](int j) {  // the box's row in the tensor map; -1: nothing to fetch
+    const int key = kN * tiles.at(i0 + j) + box_row, last = key + a.box_rows - 1;
+    if (lane >= kN / a.box_rows * kPanels || key > p_hi ||
+        (last <= p_lo - a.window && key >= a.sinks))
+      return -1;
+    if (a.n_pad > 0) return (u.pair - a.pair0) * a.n_pad + key;
+    const int page = page_of(key);
+    if (page < 0) return -1;
+    return (page * a.b.h_kv + head) * a.b.page_tokens + key % a.b.page_tokens;
+  };
+  int next_box = warp == kTmaWarp && nt > 0 ? place(0) : -1;
+  auto load = [&](int j) {
+    const int at = next_box;
+    if (j + 1 < nt) next_box = place(j + 1);
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, at >= 0));
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const int x = 2 * j + side, st = x % kStages;
+      if (x >= kStages && !warp_wait(kv_empty(st), (x / kStages - 1) & 1)) return false;
+      if (lane == 0) mbar_expect(kv_full(st), n * a.box_rows * 128);
+      __syncwarp();
+      if (at >= 0)
+        tma_box(ring + st * kTile + box_panel * kPanel + box_row * 128, side ? &map_v : &map_k,
+                64 * box_panel, at, kv_full(st));
+    }
+    return true;
+  };
+  // the first tiles are on their way while the block sets up
+  if (warp == kTmaWarp) {
+    __syncwarp();
+    for (int j = 0; j < kStages / 2 && j < nt; ++j) load(j);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -332,10 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t t_s = tmem;
   auto t_p = [&](int i) { return tmem + kN + kN / 2 * i; };
   auto t_o = [&](int i) { return tmem + 2 * kN + D * i; };
-  // the page of the token `key`, -1 where there is none
-  auto page_of = [&](int key) {
-    return key < q.len ? kv_page(a.b, s, (int)((unsigned)key / (unsigned)a.b.page_tokens)) : -1;
-  };
   // whether some row of the unit sees the key
   auto seen_by_some = [&](int key) {
     return key <= p_hi && (key > p_lo - a.window || key < a.sinks);
@@ -348,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int m = warp / 4, r = tid % kM;  // tile and row
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int c = c0 + m * kM + r;
-    const int pos = first + min(c, c1 - 1) / a.G;
+    const int pos = first + cols.row + cols.row_of(min(c, c1 - 1) - c0);
     const float cs = fmaxf(fabsf(a.qscale), 1e-37f);  // (0 would make NaN of a masked score)
     float ref = -INFINITY, l = 0.0f;
     bool live = true;
@@ -482,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---------------------------------------------------------- epilogue --
     if (m < n_m && live) {
-      const int row = q.row0 + c / a.G, h = head * a.G + c % a.G;
+      const int row = q.row0 + cols.row + cols.row_of(c - c0), h = head * a.G + cols.head_of(c - c0);
       const int64_t rh = (int64_t)row * a.h_q + h;
       const bool mine = c < c1;
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
@@ -525,11 +580,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           const int rr = 32 * (warp & 3) + (32 * i + lane) / (D / 8), ch = lane % (D / 8);
-          const int cc = c0 + m * kM + rr;
-          if (cc < c1) {
+          const int x0 = m * kM + rr;
+          if (c0 + x0 < c1) {
             const uint4 x = ld_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 +
                                         (((ch % 8) ^ (rr & 7)) << 4));
-            const int64_t at = (int64_t)(q.row0 + cc / a.G) * a.h_q + head * a.G + cc % a.G;
+            const int64_t at = (int64_t)(q.row0 + cols.row + cols.row_of(x0)) * a.h_q +
+                               head * a.G + cols.head_of(x0);
             if (a.out_wide) {
               *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + 8 * ch) = x;
             } else {
@@ -553,41 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_down<kOtherRegs>();
     if (warp == kTmaWarp && nt > 0) {
       // ----------------------------------------------------------- loads --
-      // a lane per box: box_rows rows of one page, 64 dimensions
-      constexpr int kPanels = D / 64;
-      const int boxes = kN / a.box_rows * kPanels;
-      const int row = lane / kPanels * a.box_rows, panel = lane % kPanels;
-      const bool widened = a.n_pad > 0;
-      const uint32_t bytes = (uint32_t)a.box_rows * 128;
-      const uint32_t to = ring + panel * kPanel + row * 128;
-      // the box's row in the tensor map; -1 where nothing is to be fetched
-      auto place = [&](int j) {
-        const int key = kN * tiles.at(i0 + j) + row, last = key + a.box_rows - 1;
-        if (lane >= boxes || key > p_hi || (last <= p_lo - a.window && key >= a.sinks)) return -1;
-        if (widened) return (u.pair - a.pair0) * a.n_pad + key;
-        const int page = page_of(key);
-        if (page < 0) return -1;
-        return (page * a.b.h_kv + head) * a.b.page_tokens + key % a.b.page_tokens;
-      };
       bool live = true;
-      int y = place(0);
-      for (int j = 0; j < nt && live; ++j) {
-        const int at = y;
-        if (j + 1 < nt) y = place(j + 1);
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, at >= 0));
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const int x = 2 * j + side, st = x % kStages;
-          if (x >= kStages && !warp_wait(kv_empty(st), (x / kStages - 1) & 1)) {
-            live = false;
-            s_fault = 1;
-            break;
-          }
-          if (lane == 0) mbar_expect(kv_full(st), n * bytes);
-          __syncwarp();
-          if (at >= 0) tma_box(to + st * kTile, side ? &map_v : &map_k, 64 * panel, at, kv_full(st));
-        }
-      }
+      for (int j = kStages / 2; j < nt && live; ++j) live = load(j);
+      if (!live) s_fault = 1;
       // no copy may be on its way when the block ends: the last ones are waited for
       // by their readers, or here when those have given up
       if (!live)
