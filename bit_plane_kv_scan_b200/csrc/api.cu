@@ -281,6 +281,7 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   p.b = kv_batch_of(a->cache, a->batch);
   p.h_q = a->h_q;
   p.G = a->h_q / a->cache.h_kv;
+  p.d = a->cache.d;
   p.q_bf16 = a->q_dtype == FATHOM_BF16;
   p.q_stride = a->q_stride ? a->q_stride : (int64_t)a->h_q * a->cache.d;
   p.qscale = a->softmax_scale * 1.4426950408889634f;
@@ -291,7 +292,7 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   if ((int64_t)a->batch.max_rows * p.G > FATHOM_KV_MAX_LEN)
     return fail(FATHOM_ERR_UNSUPPORTED, "max_rows=%d times %d heads a KV head is too many",
                 a->batch.max_rows, p.G);
-  plan_kv_attention(p, a->cache.d, a->cache.dtype == FATHOM_E4M3);
+  plan_kv_attention(p, a->cache.dtype == FATHOM_E4M3);
   if ((double)p.b.num_seqs * p.b.h_kv * p.col_tiles * p.splits >= 2147483647.0)
     return fail(FATHOM_ERR_UNSUPPORTED,
                 "num_seqs=%d max_rows=%d h_q=%d: too many blocks for one launch", p.b.num_seqs,
@@ -743,8 +744,7 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   p.part_ml = reinterpret_cast<float2 *>(base + w.off_ml);
   p.part_o = reinterpret_cast<float *>(base + w.off_o);
   p.wide = reinterpret_cast<const uint16_t *>(base + w.off_wide);
-  cudaError_t e = launch_kv_attention(p, a->cache.d, a->cache.dtype == FATHOM_E4M3,
-                                      (cudaStream_t)stream);
+  cudaError_t e = launch_kv_attention(p, a->cache.dtype == FATHOM_E4M3, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
   return ok();
 }

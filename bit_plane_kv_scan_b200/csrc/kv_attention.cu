@@ -632,7 +632,7 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
   const dim3 block(kThreads);
   cudaError_t e;
   if (a.many_rows)
-    e = launch_kv_prompt(a, D, f8, s);
+    e = launch_kv_prompt(a, f8, s);
   else if (f8)
     e = a.q_bf16 ? launch_ring<D, true>(kv_attention_kernel<D, true, 1>, blocks, a, s)
                  : launch_ring<D, true>(kv_attention_kernel<D, true, 2>, blocks, a, s);
@@ -644,7 +644,7 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
     e = launch_dependent(kv_combine_kernel<D>, dim3((unsigned)rh), block, 0, s, a,
                          f8 && !a.many_rows ? 15.0f : 0.0f);
   }
-  if constexpr (D == 64 || D == 128)
+  if constexpr (D >= 64)
     if (e == cudaSuccess && a.many_rows)
       e = f8 ? launch_redo<D, true>(a, s) : launch_redo<D, false>(a, s);
   return e;
@@ -661,12 +661,13 @@ static int kv_resident_blocks(int d, bool f8) {
   return 148 * (per > 4 ? 4 : per);
 }
 
-void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
-  // The tcgen05 kernel multiplies 256 columns at a time: it takes over where
-  // sequences have 64 columns or more and the queries are bf16.  (Its tensor map
+void plan_kv_attention(KvAttnParams &a, bool f8) {
+  const int d = a.d;
+  // The tcgen05 kernel multiplies 256 columns at a time (128 beyond 128 dimensions):
+  // it takes over where sequences have 64 columns or more and the queries are bf16.  (Its tensor map
   // counts the cache's rows in 31 bits.)
   const int64_t rows = (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
-  a.many_rows = a.q_bf16 && (d == 64 || d == 128) && (int64_t)a.b.max_rows * a.G >= 64 &&
+  a.many_rows = a.q_bf16 && d >= 64 && (int64_t)a.b.max_rows * a.G >= 64 &&
                 a.G <= 4096 && (f8 || rows < ((int64_t)1 << 31));
   const int64_t all_pairs = (int64_t)a.b.num_seqs * a.b.h_kv;
   a.pair0 = 0;
@@ -682,7 +683,7 @@ void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
   } else if (a.many_rows) {
     while (a.b.page_tokens % a.box_rows) a.box_rows /= 2;
   }
-  a.cols = a.many_rows ? kPromptCols : kCols;
+  a.cols = a.many_rows ? prompt_cols(d) : kCols;
   a.tile = a.many_rows ? kPromptTile : kKvBlock;
   a.col_tiles = (int)(((int64_t)a.b.max_rows * a.G + a.cols - 1) / a.cols);
   // the most tiles that one unit's columns can see
@@ -729,8 +730,8 @@ void plan_kv_attention(KvAttnParams &a, int d, bool f8) {
   a.splits = (int)((most + a.tiles_per_split - 1) / a.tiles_per_split);
 }
 
-cudaError_t launch_kv_attention(const KvAttnParams &a, int d, bool f8, cudaStream_t s) {
-  switch (d / 32) {
+cudaError_t launch_kv_attention(const KvAttnParams &a, bool f8, cudaStream_t s) {
+  switch (a.d / 32) {
     case 1: return launch_d<32>(a, f8, s);
     case 2: return launch_d<64>(a, f8, s);
     case 3: return launch_d<96>(a, f8, s);

@@ -8,8 +8,9 @@
 
 namespace fathom {
 
-// The many-rows kernel's unit: two tiles of 128 columns, against 128 keys at a time.
-constexpr int kPromptCols = 256;
+// The many-rows kernel's unit: one or two tiles of 128 columns, against 128 keys at
+// a time.
+constexpr int prompt_cols(int d) { return d <= 128 ? 256 : 128; }
 constexpr int kPromptTile = 128;
 
 struct KvAttnParams {
@@ -20,7 +21,7 @@ struct KvAttnParams {
   int64_t q_stride;
   int q_bf16;  // and out's type
   int q_wide, out_wide;  // 16-byte accesses of q's and out's rows are aligned
-  int h_q, G;
+  int h_q, G, d;
   float qscale;       // softmax scale * log2(e)
   int window, sinks;  // window: above max_len where there is none
   void *out;
@@ -103,9 +104,9 @@ __device__ __forceinline__ void write_status(const KvAttnParams &a) {
 }
 
 // kv_attention.cu
-cudaError_t launch_kv_attention(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
-void plan_kv_attention(KvAttnParams &a, int d, bool f8);
+cudaError_t launch_kv_attention(const KvAttnParams &a, bool f8, cudaStream_t s);
+void plan_kv_attention(KvAttnParams &a, bool f8);
 // kv_prompt.cu: the tcgen05 kernel, and the widening before it
-cudaError_t launch_kv_prompt(const KvAttnParams &a, int d, bool f8, cudaStream_t s);
+cudaError_t launch_kv_prompt(const KvAttnParams &a, bool f8, cudaStream_t s);
 
 }  // namespace fathom

@@ -2,7 +2,7 @@
 // over the paged cache on the tcgen05 tensor cores.
 //
 // A unit is 256 (token, head) pairs of one sequence and KV head, as two tiles
-// of 128 rows: the G heads that share a KV head share its keys.  One
+// of 128 rows (one, beyond 128 dimensions): the G heads that share a KV head share its keys.  One
 // thread block per SM takes a unit through its keys, 128 at a time:
 //   S = Q_i K^T        tcgen05.mma, Q and K in shared memory, S in tensor memory
 //   P_i = 2^(c S - m_i)     one thread a row, from registers, rounded to bf16
@@ -54,22 +54,27 @@ constexpr int kSoftRegs = 224, kOtherRegs = 56;
 static_assert(kSoftRegs * 256 + kOtherRegs * 128 <= 168 * kThreads, "registers of the block");
 constexpr int kM = 128;                  // rows of a tile
 constexpr int kN = kPromptTile;          // keys of a tile
-constexpr int kStages = 4;               // ring of K and V tiles
 constexpr int kPanel = kM * 128;         // bytes of 64 dimensions of 128 rows
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.0f;           // a row's reference lags its maximum by less
 
-template <int D>
-constexpr int tile_bytes() { return D / 64 * kPanel; }
-
-// Shared memory: Q's two tiles, then the ring; 1024-byte aligned (the swizzle's
-// period).  More than half an SM's, so that two blocks never share an SM and its
-// tensor memory.
-template <int D>
-constexpr int smem_bytes() {
-  const int b = (2 + kStages) * tile_bytes<D>() + 1024;
-  return b < 120 * 1024 ? 120 * 1024 : b;
-}
+// A kernel is made for DP = 64, 128 or 256 dimensions, or (not FULL, which costs 3%)
+// for fewer than 128 or 256.  (TMA fills the boxes
+// past d with zeros; products go over d dimensions alone.)  Up to 128 a unit has
+// two row tiles and the ring four places; at 256 tensor memory has room for one O
+// and shared memory for one tile of Q and a ring of two.
+template <int DP>
+struct Size {
+  static constexpr int kTiles = DP <= 128 ? 2 : 1;
+  static constexpr int kStages = DP <= 128 ? 4 : 2;
+  static constexpr int kTileBytes = DP / 64 * kPanel;
+  // Q's tiles, then the ring; 1024-byte aligned (the swizzle's period).  More than
+  // half an SM's, so that two blocks never share an SM and its tensor memory.
+  static constexpr int kBytes = (kTiles + kStages) * kTileBytes + 1024;
+  static constexpr int kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;
+};
+static_assert(Size<256>::kTiles * 128 == prompt_cols(256) && Size<128>::kTiles * 128 == prompt_cols(128),
+              "units as the plan has them");
 
 // 128-byte swizzle.  K-major (Q, K): 8-row groups 1024 bytes apart.  MN-major
 // (V, whose rows are the contracted keys): 8-key groups 1024 bytes apart, groups
@@ -248,12 +253,13 @@ __host__ __device__ __forceinline__ int unit_blocks(const KvAttnParams &a) {
   return units - tail + tail * a.splits;
 }
 
-template <int D>
+template <int DP, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_prompt_kernel(const __grid_constant__ KvAttnParams a, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
-  constexpr int kTile = tile_bytes<D>();
-  constexpr int kSteps = D / 16;
+  constexpr int kTile = Size<DP>::kTileBytes, kTiles = Size<DP>::kTiles, kStages = Size<DP>::kStages;
+  constexpr int kChunks = DP / 8;  // 16-byte pieces of a row in shared memory
+  const int d = FULL ? DP : a.d;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[3 * kStages + 12];
   __shared__ uint32_t s_tmem;
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *taint = a.taint + ((int64_t)u.pair * a.col_tiles + rb) * a.splits + split;
   if (tid < (u.splits == 1 ? a.splits : 1)) taint[tid] = 0;
   const KvSeq q = kv_seq(a.b, s);
-  const int c0 = rb * kPromptCols, c1 = min(c0 + kPromptCols, q.rows * a.G);
+  const int c0 = rb * kM * kTiles, c1 = min(c0 + kM * kTiles, q.rows * a.G);
   if (c0 >= c1) return;
   const int first = q.len - q.rows;  // position of the sequence's first row
   const int p_lo = first + c0 / a.G, p_hi = first + (c1 - 1) / a.G;
@@ -283,31 +289,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_m = c1 - c0 > kM ? 2 : 1;  // tiles of rows
   const Columns cols(c0, a.G);
 
-  // The softmax warps' 32 rows of Q each (zeros behind the last), a row by 16 or 8
-  // lanes: all on their way while the block sets up, looked at afterwards.
-  uint4 xq[D / 8];
-  if (warp < kSoftWarps && nt > 0) {
-    const uint16_t *rows = static_cast<const uint16_t *>(a.q) + 8 * (lane % (D / 8));
-    auto row_of = [&](int i) {  // a row behind the last: the last
-      const int x = min(32 * warp + (32 * i + lane) / (D / 8), c1 - 1 - c0);
-      return rows + (int64_t)(q.row0 + cols.row + cols.row_of(x)) * a.q_stride +
-             (head * a.G + cols.head_of(x)) * D;
-    };
-    if (a.q_wide) {
+  // The softmax warps' 32 rows of Q each (zeros behind the last), a row by 8 to 32
+  // lanes: 16 loads on their way while the block sets up, looked at afterwards.
+  constexpr int kEarly = kChunks < 16 ? kChunks : 16;
+  uint4 xq[kEarly];
+  auto load_q = [&](int i) {  // a row behind the last: the last; dimensions past d: zeros
+    const int x = min(32 * warp + (32 * i + lane) / kChunks, c1 - 1 - c0), ch = lane % kChunks;
+    if (8 * ch >= d) return make_uint4(0, 0, 0, 0);
+    const uint16_t *e = static_cast<const uint16_t *>(a.q) +
+                        (int64_t)(q.row0 + cols.row + cols.row_of(x)) * a.q_stride +
+                        (head * a.G + cols.head_of(x)) * d + 8 * ch;
+    if (a.q_wide) return __ldg(reinterpret_cast<const uint4 *>(e));
+    return make_uint4(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16),
+                      e[4] | ((uint32_t)e[5] << 16), e[6] | ((uint32_t)e[7] << 16));
+  };
+  if (warp < 4 * kTiles && nt > 0)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) xq[i] = __ldg(reinterpret_cast<const uint4 *>(row_of(i)));
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint16_t *e = row_of(i);
-        xq[i] = make_uint4(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16),
-                           e[4] | ((uint32_t)e[5] << 16), e[6] | ((uint32_t)e[7] << 16));
-      }
-    }
-  }
+    for (int i = 0; i < kEarly; ++i) xq[i] = load_q(i);
 
   const uint32_t base = (tc_smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sq = base, ring = base + 2 * kTile;
+  const uint32_t sq = base, ring = base + kTiles * kTile;
   const uint32_t bar0 = tc_smem_u32(s_bar);
   auto kv_full = [&](int i) { return bar0 + 8 * i; };                  // TMA's bytes are there
   auto kv_empty = [&](int i) { return bar0 + 8 * (kStages + i); };     // the MMAs are done with it
@@ -349,11 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // K and V of tile j into the ring, by the TMA warp: a lane per box (box_rows rows of
   // one page, 64 dimensions).  False if the ring's places did not become free.
-  constexpr int kPanels = D / 64;
-  const int box_row = lane / kPanels * a.box_rows, box_panel = lane % kPanels;
+  const int panels = (d + 63) / 64;
+  const int box_row = lane / panels * a.box_rows, box_panel = lane % panels;
   auto place = [&](int j) {  // the box's row in the tensor map; -1: nothing to fetch
     const int key = kN * tiles.at(i0 + j) + box_row, last = key + a.box_rows - 1;
-    if (lane >= kN / a.box_rows * kPanels || key > p_hi ||
+    if (lane >= kN / a.box_rows * panels || key > p_hi ||
         (last <= p_lo - a.window && key >= a.sinks))
       return -1;
     if (a.n_pad > 0) return (u.pair - a.pair0) * a.n_pad + key;
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tensor memory: S (of one tile at a time), P_0, P_1, O_0, O_1
   const uint32_t t_s = tmem;
   auto t_p = [&](int i) { return tmem + kN + kN / 2 * i; };
-  auto t_o = [&](int i) { return tmem + 2 * kN + D * i; };
+  auto t_o = [&](int i) { return tmem + 2 * kN + DP * i; };
   // whether some row of the unit sees the key
   auto seen_by_some = [&](int key) {
     return key <= p_hi && (key > p_lo - a.window || key < a.sinks);
@@ -409,16 +410,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool live = true;
     if (nt > 0 && m < n_m) {
       const uint32_t flip = a.qscale < 0.0f ? 0x80008000u : 0u;  // makes the scale positive
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const int rr = 32 * (warp & 3) + (32 * i + lane) / (D / 8), ch = lane % (D / 8);
-        uint4 x = xq[i];
+      auto store_q = [&](int i, uint4 x) {
+        const int rr = 32 * (warp & 3) + (32 * i + lane) / kChunks, ch = lane % kChunks;
         x.x ^= flip;
         x.y ^= flip;
         x.z ^= flip;
         x.w ^= flip;
         if (c0 + m * kM + rr >= c1) x = make_uint4(0, 0, 0, 0);
         st_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 + (((ch % 8) ^ (rr & 7)) << 4), x);
+      };
+#pragma unroll
+      for (int i = 0; i < kEarly; ++i) store_q(i, xq[i]);
+      if constexpr (kChunks > kEarly) {
+#pragma unroll
+        for (int i = 0; i < kChunks - kEarly; ++i) xq[i] = load_q(kEarly + i);
+#pragma unroll
+        for (int i = 0; i < kChunks - kEarly; ++i) store_q(kEarly + i, xq[i]);
       }
       proxy_fence();
       mbar_arrive(q_full(m));
@@ -494,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ref = next;
           if (j > 0) {  // (tile 0 overwrites O)
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
+            for (int i = 0; i < DP / 16; ++i) {
+              if (16 * i >= d) break;
               uint32_t o[16];
               tc_ld16(t_o(m) + lanes + 16 * i, o);
               tc_wait_ld();
@@ -543,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
       const int64_t part = (int64_t)split * a.b.num_rows * a.h_q + rh;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+      for (int i = 0; i < DP / 32; ++i) {
+        if (32 * i >= d) break;
         uint32_t v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = 0u;
@@ -566,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         make_uint4(w[0], w[1], w[2], w[3]));
           }
         } else if (mine) {
-          float *out = a.part_o + part * D + 32 * i;
+          float *out = a.part_o + part * d + 32 * i;
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4 *>(out + e) =
@@ -578,21 +587,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u.splits == 1) {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const int rr = 32 * (warp & 3) + (32 * i + lane) / (D / 8), ch = lane % (D / 8);
+        for (int i = 0; i < kChunks; ++i) {
+          const int rr = 32 * (warp & 3) + (32 * i + lane) / kChunks, ch = lane % kChunks;
           const int x0 = m * kM + rr;
-          if (c0 + x0 < c1) {
+          if (c0 + x0 < c1 && 8 * ch < d) {
             const uint4 x = ld_shared16(sq + m * kTile + (ch / 8) * kPanel + rr * 128 +
                                         (((ch % 8) ^ (rr & 7)) << 4));
             const int64_t at = (int64_t)(q.row0 + cols.row + cols.row_of(x0)) * a.h_q +
                                head * a.G + cols.head_of(x0);
             if (a.out_wide) {
-              *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + 8 * ch) = x;
+              *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * d + 8 * ch) = x;
             } else {
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int z = 0; z < 8; ++z)
-                static_cast<uint16_t *>(a.out)[at * D + 8 * ch + z] = (uint16_t)(w[z / 2] >> (16 * (z & 1)));
+                static_cast<uint16_t *>(a.out)[at * d + 8 * ch + z] = (uint16_t)(w[z / 2] >> (16 * (z & 1)));
             }
           }
         }
@@ -638,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (seen && sees_all(a, p_lo, p_hi, key, 1)) continue;
             const uint32_t at = ring + st * kTile + r * 128;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {  // (each lane starts elsewhere: other banks)
+            for (int i = 0; i < kChunks; ++i) {  // (each lane starts elsewhere: other banks)
+              if (64 * (i / 8) >= d) break;  // a panel that is not there
               const uint32_t w = at + (i / 8) * kPanel + 16 * ((i + lane) % 8);
               if (!seen) {
                 st_shared16(w, make_uint4(0, 0, 0, 0));
@@ -655,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp && nt > 0) {
       // ------------------------------------------------------------ MMAs --
-      constexpr uint32_t kIdS = idesc(kN, false), kIdO = idesc(D, true);
+      const uint32_t id_s = idesc(kN, false), id_o = idesc(d, true);
       const bool leader = tc_elect_one();
       bool live = mbar_wait(q_full(0), 0);
       if (n_m == 2 && live) live = mbar_wait(q_full(1), 0);
@@ -666,17 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto mul_s = [&](int m, int stage) {
         if (!leader) return;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        for (int k = 0; k < DP / 16; ++k) {
+          if (16 * k >= d) break;
           const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
           mma_ss(t_s, smem_desc(sq + m * kTile + off, 16), smem_desc(ring + stage * kTile + off, 16),
-                 kIdS, k > 0);
+                 id_s, k > 0);
         }
       };
       auto mul_o = [&](int m, int half, int stage, bool acc) {
         if (!leader) return;
 #pragma unroll
         for (int k = 4 * half; k < 4 * half + 4; ++k)
-          mma_ts(t_o(m), t_p(m) + 8 * k, smem_desc(ring + stage * kTile + k * 2048, kPanel), kIdO,
+          mma_ts(t_o(m), t_p(m) + 8 * k, smem_desc(ring + stage * kTile + k * 2048, kPanel), id_o,
                  acc || k > 0);
       };
       auto commit = [&](uint32_t bar) {
@@ -717,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           commit(s_full(0));
           if (n_m == 1) commit(kv_empty(st));
         }
-        if (!wait(v_ready((2 * j + 1) % kStages), (j >> 1) & 1)) break;
+        if (!wait(v_ready((2 * j + 1) % kStages), ((2 * j + 1) / kStages) & 1)) break;
         add_o(0, j);
         if (n_m == 2) {
           if (more) {
@@ -760,16 +771,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
 }
 
-// E4M3: the keys that some row sees, K and V, as bf16 in [pair - pair0][n_pad][D].  A
+// E4M3: the keys that some row sees, K and V, as bf16 in [pair - pair0][n_pad][d].  A
 // block per 128 keys of a pair; bound by bytes (1 read, 2 written an element).
 constexpr int kWidenThreads = 256;
 
-template <int D>
 __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_constant__ KvAttnParams a,
                                                               uint16_t *wide_k, uint16_t *wide_v) {
   grid_dependency_wait();
   allow_dependent_launch();
-  constexpr int kPieces = D / 16;
+  const int d = a.d, pieces = d / 16;
   const int per = a.n_pad / kN;
   const int pair = blockIdx.x / per, key0 = blockIdx.x % per * kN;
   const int head = (a.pair0 + pair) % a.b.h_kv, s = (a.pair0 + pair) / a.b.h_kv;
@@ -777,17 +787,17 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
   if (q.rows == 0 || key0 >= q.len) return;
   const int from = q.len - q.rows - a.window;  // the last key before every row's window
   if (key0 + kN - 1 <= from && key0 >= a.sinks) return;
-  for (int i = threadIdx.x; i < kN * kPieces; i += kWidenThreads) {
-    const int r = i / kPieces, piece = i % kPieces, key = key0 + r;
+  for (int i = threadIdx.x; i < kN * pieces; i += kWidenThreads) {
+    const int r = (int)((unsigned)i / (unsigned)pieces), piece = i - r * pieces, key = key0 + r;
     if (key >= q.len) return;
     const int at = (int)((unsigned)key / (unsigned)a.b.page_tokens);
     const int page = kv_page(a.b, s, at);
     if (page < 0) continue;
     const int slot = key - at * a.b.page_tokens;
     const int64_t h = (int64_t)page * a.b.h_kv + head;
-    const int64_t src = (h * a.b.page_tokens + slot) * D + piece * 16;
+    const int64_t src = (h * a.b.page_tokens + slot) * d + piece * 16;
     const int64_t sc = h * (a.b.page_tokens / kKvBlock) + slot / kKvBlock;
-    const int64_t dst = ((int64_t)pair * a.n_pad + key) * D + piece * 16;
+    const int64_t dst = ((int64_t)pair * a.n_pad + key) * d + piece * 16;
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const uint4 v = __ldg(reinterpret_cast<const uint4 *>(
@@ -829,28 +839,28 @@ cudaError_t make_map(CUtensorMap *map, const void *ptr, int64_t rows, int d, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D>
+template <int DP, bool FULL>
 cudaError_t launch(KvAttnParams a, bool f8, cudaStream_t s) {
-  constexpr int smem = smem_bytes<D>();
-  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>,
+  constexpr int smem = Size<DP>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<DP, FULL>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   CUtensorMap map_k, map_v;
   const void *k = f8 ? a.wide : a.ck;
-  const void *v = f8 ? a.wide + (size_t)a.pairs * a.n_pad * D : a.cv;
+  const void *v = f8 ? a.wide + (size_t)a.pairs * a.n_pad * a.d : a.cv;
   const int64_t rows = f8 ? (int64_t)a.pairs * a.n_pad
                           : (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
-  e = make_map(&map_k, k, rows, D, a.box_rows);
-  if (e == cudaSuccess) e = make_map(&map_v, v, rows, D, a.box_rows);
+  e = make_map(&map_k, k, rows, a.d, a.box_rows);
+  if (e == cudaSuccess) e = make_map(&map_v, v, rows, a.d, a.box_rows);
   const int all = a.b.num_seqs * a.b.h_kv, group = a.pairs;
   for (a.pair0 = 0; a.pair0 < all && e == cudaSuccess; a.pair0 += group) {
     a.pairs = all - a.pair0 < group ? all - a.pair0 : group;
     if (f8)
-      e = launch_dependent(widen_kernel<D>, dim3((unsigned)(a.pairs * (a.n_pad / kN))),
+      e = launch_dependent(widen_kernel, dim3((unsigned)(a.pairs * (a.n_pad / kN))),
                            dim3(kWidenThreads), 0, s, a, const_cast<uint16_t *>(a.wide),
                            static_cast<uint16_t *>(const_cast<void *>(v)));
     if (e == cudaSuccess)
-      e = launch_dependent(kv_prompt_kernel<D>,
+      e = launch_dependent(kv_prompt_kernel<DP, FULL>,
                            dim3((unsigned)(unit_blocks(a) + (a.pair0 == 0))),
                            dim3(kThreads), smem, s, a, map_k, map_v);
   }
@@ -859,10 +869,13 @@ cudaError_t launch(KvAttnParams a, bool f8, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_kv_prompt(const KvAttnParams &a, int d, bool f8, cudaStream_t s) {
-  if (d == 128) return launch<128>(a, f8, s);
-  if (d == 64) return launch<64>(a, f8, s);
-  return cudaErrorInvalidValue;
+cudaError_t launch_kv_prompt(const KvAttnParams &a, bool f8, cudaStream_t s) {
+  switch (a.d) {
+    case 64: return launch<64, true>(a, f8, s);
+    case 128: return launch<128, true>(a, f8, s);
+    case 256: return launch<256, true>(a, f8, s);
+    default: return a.d < 128 ? launch<128, false>(a, f8, s) : launch<256, false>(a, f8, s);
+  }
 }
 
 }  // namespace fathom

@@ -311,6 +311,25 @@ def test_attention(case, dtype, qt):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("G,page,lens,rows,window,sinks", [
+    (4, 16, [300], [150], 0, 0), (7, 48, [257, 40], [257, 11], 50, 3), (1, 128, [700, 1, 0], [129, 1, 0], 0, 0)])
+def test_attention_many_rows(d, G, page, lens, rows, window, sinks, dtype):
+    """Every width of the many-rows kernel: small and odd pages, several units and tiles,
+    ragged sequences."""
+    rng = np.random.default_rng(d + G)
+    ct = BF16 if dtype == "bf16" else F8
+    pages = sum(-(-n // page) for n in lens) + 1
+    cache = make_cache(rng, pages, page, 2, d, ct)
+    batch, table, seqs = make_batch(rng, pages, page, lens, rows)
+    q = randn(rng, batch.num_rows, 2 * G, d, scale=1.5)
+    got = F.kv_attention(cache, batch, q, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    want = R.attention(ref_cache(cache), table, seqs, R.f64(q), 1 / math.sqrt(d), window, sinks, WEIGHT[ct, BF16])
+    check_attention(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (500, 20), (3000, 0), (5000, 100)])
 def test_attention_split_over_blocks(dtype, window, sinks):
     """A context long enough that several blocks share it, with max_len far above
