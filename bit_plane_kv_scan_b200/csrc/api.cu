@@ -266,7 +266,9 @@ fathom_status check_rows(const char *name, int dtype, int heads, int d, int64_t 
 }
 
 // Everything about an attention call but its pointers, and its plan.
-fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams &p) {
+fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams (&plan)[2],
+                                 int &plans) {
+  plans = 0;
   REQUIRE(a != nullptr, "args is NULL");
   fathom_status st = check_kv_shape(a->cache, a->batch);
   if (st != FATHOM_OK) return st;
@@ -277,6 +279,7 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   REQUIRE(std::isfinite(a->softmax_scale), "softmax_scale is not finite");
   REQUIRE(a->window >= 0, "window=%lld is negative", (long long)a->window);
   REQUIRE(a->sinks >= 0, "sinks=%lld is negative", (long long)a->sinks);
+  KvAttnParams p;
   memset(&p, 0, sizeof(p));
   p.b = kv_batch_of(a->cache, a->batch);
   p.h_q = a->h_q;
@@ -288,34 +291,43 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   const int64_t all = FATHOM_KV_MAX_LEN;
   p.window = (int)(a->window == 0 || a->window > all ? all : a->window);
   p.sinks = (int)(a->sinks > all ? all : a->sinks);
-  if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return FATHOM_OK;
+  if (a->batch.max_rows == 0 || a->batch.num_seqs == 0) return FATHOM_OK;  // no rows
   if ((int64_t)a->batch.max_rows * p.G > FATHOM_KV_MAX_LEN)
     return fail(FATHOM_ERR_UNSUPPORTED, "max_rows=%d times %d heads a KV head is too many",
                 a->batch.max_rows, p.G);
-  plan_kv_attention(p, a->cache.dtype == FATHOM_E4M3);
-  if ((double)p.b.num_seqs * p.b.h_kv * p.col_tiles * p.splits >= 2147483647.0)
-    return fail(FATHOM_ERR_UNSUPPORTED,
-                "num_seqs=%d max_rows=%d h_q=%d: too many blocks for one launch", p.b.num_seqs,
-                p.b.max_rows, p.h_q);
+  plans = plan_kv_attention(p, a->cache.dtype == FATHOM_E4M3, plan);
+  for (int i = 0; i < plans; ++i)
+    if ((double)plan[i].units * p.b.h_kv * plan[i].splits >= 2147483647.0)
+      return fail(FATHOM_ERR_UNSUPPORTED,
+                  "num_seqs=%d max_rows=%d h_q=%d: too many blocks for one launch", p.b.num_seqs,
+                  p.b.max_rows, p.h_q);
+  if ((double)p.b.num_rows * p.h_q >= 2147483647.0)
+    return fail(FATHOM_ERR_UNSUPPORTED, "num_rows=%d times h_q=%d is too many", p.b.num_rows, p.h_q);
   return FATHOM_OK;
 }
 
-// The workspace: status, the units' marks, the splits' maxima and sums and their
-// outputs, then the widened keys and values.
-struct KvWorkspace {
-  size_t off_taint, off_ml, off_o, off_wide, total;
-};
-
-KvWorkspace kv_workspace(const KvAttnParams &p, int d) {
-  const size_t parts = p.splits > 1 ? (size_t)p.splits * p.b.num_rows * p.h_q : 0;
-  const size_t marks = p.many_rows ? (size_t)p.b.num_seqs * p.b.h_kv * p.col_tiles * p.splits : 0;
-  KvWorkspace w;
-  w.off_taint = sizeof(WsStatus);
-  w.off_ml = w.off_taint + up256(marks * 4);
-  w.off_o = w.off_ml + up256(parts * 8);
-  w.off_wide = w.off_o + up256(parts * d * 4);
-  w.total = w.off_wide + (size_t)(p.many_rows ? p.pairs : 0) * p.n_pad * d * 4;
-  return w;
+// The workspace: status, then for each launch the units' marks, the splits' maxima
+// and sums and their outputs, and the widened keys and values.  Returns its size; with
+// a base address, the launches learn where their parts are.
+size_t kv_workspace(KvAttnParams (&plan)[2], int plans, unsigned char *base) {
+  size_t at = sizeof(WsStatus);
+  for (int i = 0; i < plans; ++i) {
+    KvAttnParams &p = plan[i];
+    const size_t parts = p.splits > 1 ? (size_t)p.splits * p.b.num_rows * p.h_q : 0;
+    const size_t marks = p.many_rows ? (size_t)p.units * p.b.h_kv * p.splits : 0;
+    if (base) {
+      p.status = reinterpret_cast<WsStatus *>(base);
+      p.taint = reinterpret_cast<int *>(base + at);
+    }
+    at += up256(marks * 4);
+    if (base) p.part_ml = reinterpret_cast<float2 *>(base + at);
+    at += up256(parts * 8);
+    if (base) p.part_o = reinterpret_cast<float *>(base + at);
+    at += up256(parts * p.d * 4);
+    if (base) p.wide = reinterpret_cast<const uint16_t *>(base + at);
+    at += (size_t)(p.many_rows ? p.pairs : 0) * p.n_pad * p.d * 4;
+  }
+  return at;
 }
 
 }  // namespace
@@ -680,7 +692,7 @@ fathom_status fathom_kv_append(const fathom_kv_append_args *a, void *stream) {
   REQUIRE(a->rotary_pairs >= 0 && 2 * (int64_t)a->rotary_pairs <= d,
           "rotary_pairs=%d out of range [0, d/2=%d]", a->rotary_pairs, d / 2);
   REQUIRE(a->rotary_pairs == 0 || a->inv_freq != nullptr, "inv_freq is NULL");
-  if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return ok();
+  if (a->batch.max_rows == 0 || a->batch.num_seqs == 0) return ok();  // no rows
   const int dev = current_device();
   st = check_kv_pointers(a->cache, a->batch, dev);
   if (st != FATHOM_OK) return st;
@@ -705,18 +717,20 @@ fathom_status fathom_kv_append(const fathom_kv_append_args *a, void *stream) {
 }
 
 size_t fathom_kv_attention_workspace_size(const fathom_kv_attention_args *a) {
-  KvAttnParams p;
-  if (check_kv_attention(a, p) != FATHOM_OK) return 0;
-  return kv_workspace(p, a->cache.d).total;
+  KvAttnParams plan[2];
+  int plans;
+  if (check_kv_attention(a, plan, plans) != FATHOM_OK) return 0;
+  return kv_workspace(plan, plans, nullptr);
 }
 
 fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, size_t ws_bytes,
                                   void *stream) {
   const CallRange range("fathom_kv_attention");
-  KvAttnParams p;
-  fathom_status st = check_kv_attention(a, p);
+  KvAttnParams plan[2];
+  int plans;
+  fathom_status st = check_kv_attention(a, plan, plans);
   if (st != FATHOM_OK) return st;
-  if (a->batch.num_rows == 0 || a->batch.num_seqs == 0) return ok();
+  if (plans == 0) return ok();  // no sequences or no rows
   const int dev = current_device();
   st = check_kv_pointers(a->cache, a->batch, dev);
   if (st != FATHOM_OK) return st;
@@ -725,27 +739,24 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   REQUIRE_ON_DEVICE(a->out, "out", el);
   if (a->lse) REQUIRE_ON_DEVICE(a->lse, "lse", 4);
   REQUIRE_ON_DEVICE(ws, "workspace", 256);
-  const KvWorkspace w = kv_workspace(p, a->cache.d);
-  if (ws_bytes < w.total)
-    return fail(FATHOM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes,
-                w.total);
-  p.ck = a->cache.k;
-  p.cv = a->cache.v;
-  p.k_scale = a->cache.k_scale;
-  p.v_scale = a->cache.v_scale;
-  p.q = a->q;
-  p.q_wide = aligned(a->q, 16) && p.q_stride % (p.q_bf16 ? 8 : 4) == 0;
-  p.out_wide = aligned(a->out, 16);
-  p.out = a->out;
-  p.lse = a->lse;
-  unsigned char *base = static_cast<unsigned char *>(ws);
-  p.status = reinterpret_cast<WsStatus *>(base);
-  p.taint = reinterpret_cast<int *>(base + w.off_taint);
-  p.part_ml = reinterpret_cast<float2 *>(base + w.off_ml);
-  p.part_o = reinterpret_cast<float *>(base + w.off_o);
-  p.wide = reinterpret_cast<const uint16_t *>(base + w.off_wide);
-  cudaError_t e = launch_kv_attention(p, a->cache.dtype == FATHOM_E4M3, (cudaStream_t)stream);
-  if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
+  const size_t need = kv_workspace(plan, plans, static_cast<unsigned char *>(ws));
+  if (ws_bytes < need)
+    return fail(FATHOM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  for (int i = 0; i < plans; ++i) {
+    KvAttnParams &p = plan[i];
+    p.ck = a->cache.k;
+    p.cv = a->cache.v;
+    p.k_scale = a->cache.k_scale;
+    p.v_scale = a->cache.v_scale;
+    p.q = a->q;
+    p.q_wide = aligned(a->q, 16) && p.q_stride % (p.q_bf16 ? 8 : 4) == 0;
+    p.out = a->out;
+    p.out_wide = aligned(a->out, 16);
+    p.lse = a->lse;
+    const cudaError_t e =
+        launch_kv_attention(p, a->cache.dtype == FATHOM_E4M3, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
+  }
   return ok();
 }
 

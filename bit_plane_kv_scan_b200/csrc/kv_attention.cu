@@ -204,8 +204,9 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
   float(*s_o)[kCols][D + 4] = reinterpret_cast<float(*)[kCols][D + 4]>(s_ring);
   static_assert(sizeof(float) * kWarps * kCols * (D + 4) <= S::kSmem, "outputs fit in the rings");
   const KvSeq q = kv_seq(a.b, s);
-  const int c0 = ct * kCols, c1 = min(c0 + kCols, q.rows * a.G);  // columns of this block
-  if (c0 >= c1) return;
+  // columns of this block (ct may be past the sequence's last)
+  const int c1 = (int)min((int64_t)(ct + 1) * kCols, (int64_t)q.rows * a.G), c0 = ct * kCols;
+  if (c0 >= c1 || !owns(a, q)) return;
   const int first = q.len - q.rows;  // position of the sequence's first row
   const int p_lo = first + c0 / a.G, p_hi = first + (c1 - 1) / a.G;
   const KvTiles tiles = visible_tiles(a, p_lo, p_hi, kKvBlock);
@@ -490,16 +491,15 @@ __global__ void __launch_bounds__(kThreads, F8 && TERMS == 1 && D <= 128 ? 4 : 1
     kv_attention_kernel(KvAttnParams a) {
   grid_dependency_wait();
   allow_dependent_launch();
-  if (blockIdx.x == gridDim.x - 1) {
+  int x = blockIdx.x;
+  if (x == a.units * a.b.h_kv * a.splits) {  // one more, if it reports
     write_status(a);
     return;
   }
-  int x = blockIdx.x;
   const int split = x % a.splits;
   x /= a.splits;
-  const int ct = x % a.col_tiles;
-  x /= a.col_tiles;
-  attend<D, F8, TERMS>(a, x / a.b.h_kv, x % a.b.h_kv, ct, split);
+  const KvUnit u = kv_unit(a, x / a.b.h_kv);
+  attend<D, F8, TERMS>(a, u.s, x % a.b.h_kv, u.ct, split);
 }
 
 // After the many-rows kernel: the units that it marked, column tile by column
@@ -508,18 +508,26 @@ template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const int per = a.cols / kCols, units = a.b.num_seqs * a.b.h_kv * a.col_tiles;
+  const int per = a.cols / kCols, units = a.units * a.b.h_kv;
   KvAttnParams b = a;
   b.splits = 1;
   b.tiles_per_split = 1 << 30;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int x0 = blockIdx.x * kThreads; x0 < units; x0 += gridDim.x * kThreads) {
+    // a thread looks at one unit's marks; marked ones are rare
     int marked = 0;
-    for (int i = threadIdx.x; i < a.splits; i += kThreads) marked |= a.taint[(int64_t)u * a.splits + i];
+    if (x0 + (int)threadIdx.x < units)
+      for (int i = 0; i < a.splits; ++i)
+        marked |= a.taint[(int64_t)(x0 + threadIdx.x) * a.splits + i];
     if (!__syncthreads_or(marked)) continue;
-    const int rb = u % a.col_tiles, x = u / a.col_tiles;
-    for (int ct = 0; ct < per; ++ct) {
-      attend<D, F8, 1>(b, x / b.b.h_kv, x % b.b.h_kv, rb * per + ct, 0);
-      __syncthreads();
+    for (int k = 0; k < kThreads; ++k) {
+      if (!__syncthreads_or(marked && (int)threadIdx.x == k)) continue;
+      const KvUnit u = kv_unit(a, (x0 + k) / a.b.h_kv);
+      const KvSeq q = kv_seq(a.b, u.s);
+      const int rb = (q.rows * a.G + a.cols - 1) / a.cols - 1 - u.ct;  // (units come last first)
+      for (int ct = 0; ct < per; ++ct) {
+        attend<D, F8, 1>(b, u.s, (x0 + k) % a.b.h_kv, rb * per + ct, 0);
+        __syncthreads();
+      }
     }
   }
 }
@@ -538,11 +546,12 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, fl
   const int row = (int)(rh / a.h_q), h = (int)(rh % a.h_q);
   const int s = a.b.q_start ? find_seq(a.b.num_seqs, row, [&](int i) { return a.b.q_start[i]; }) : row;
   const KvSeq q = kv_seq(a.b, s);
-  if (row < q.row0 || row >= q.row0 + q.rows) return;
+  if (row < q.row0 || row >= q.row0 + q.rows || !owns(a, q)) return;
   const int col = (row - q.row0) * a.G + h % a.G, c0 = col / a.cols * a.cols;
-  // (many rows: the unit's number in order of work; those before tail_from are whole)
+  // (many rows of one sequence: the unit's number in order of work; those before
+  // tail_from are whole)
   if (a.tail_from > 0 &&
-      (a.col_tiles - 1 - col / a.cols) * a.pairs + s * a.b.h_kv + h / a.G < a.tail_from)
+      ((q.rows * a.G - 1) / a.cols - col / a.cols) * a.b.h_kv + h / a.G < a.tail_from)
     return;
   const int c1 = min(c0 + a.cols, q.rows * a.G), first = q.len - q.rows;
   const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
@@ -622,13 +631,13 @@ cudaError_t launch_ring(Kernel kernel, int64_t blocks, const KvAttnParams &a, cu
 
 template <int D, bool F8>
 cudaError_t launch_redo(const KvAttnParams &a, cudaStream_t s) {
-  const int units = a.b.num_seqs * a.b.h_kv * a.col_tiles;
-  return launch_ring<D, F8>(kv_redo_kernel<D, F8>, units < 296 ? units : 296, a, s);
+  const int64_t blocks = ((int64_t)a.units * a.b.h_kv + kThreads - 1) / kThreads;
+  return launch_ring<D, F8>(kv_redo_kernel<D, F8>, blocks < 296 ? blocks : 296, a, s);
 }
 
 template <int D>
 cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
-  const int64_t blocks = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles * a.splits + 1;
+  const int64_t blocks = (int64_t)a.units * a.b.h_kv * a.splits + a.report;
   const dim3 block(kThreads);
   cudaError_t e;
   if (a.many_rows)
@@ -661,31 +670,33 @@ static int kv_resident_blocks(int d, bool f8) {
   return 148 * (per > 4 ? 4 : per);
 }
 
-void plan_kv_attention(KvAttnParams &a, bool f8) {
+// One launch's plan: of the few-rows or the many-rows kernel, for a.own's sequences.
+static void plan_one(KvAttnParams &a, bool f8) {
   const int d = a.d;
-  // The tcgen05 kernel multiplies 256 columns at a time (128 beyond 128 dimensions):
-  // it takes over where sequences have 64 columns or more and the queries are bf16.  (Its tensor map
-  // counts the cache's rows in 31 bits.)
-  const int64_t rows = (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
-  a.many_rows = a.q_bf16 && d >= 64 && (int64_t)a.b.max_rows * a.G >= 64 &&
-                a.G <= 4096 && (f8 || rows < ((int64_t)1 << 31));
+  int64_t max_cols = (int64_t)a.b.max_rows * a.G;
+  if (a.own == kFewRows && max_cols >= kManyCols) max_cols = kManyCols - 1;
   const int64_t all_pairs = (int64_t)a.b.num_seqs * a.b.h_kv;
   a.pair0 = 0;
   a.pairs = (int)all_pairs;
   a.n_pad = 0;
   a.box_rows = kPromptTile;
   if (a.many_rows && f8) {
-    // The widened copy holds as many pairs at a time as fit in 1 GiB.
+    // The widened copy holds as many pairs at a time as fit in 4 GiB.
     a.n_pad = (int)(((int64_t)a.b.max_len + kPromptTile - 1) / kPromptTile * kPromptTile);
     if (a.n_pad == 0) a.n_pad = kPromptTile;
-    const int64_t fit = ((int64_t)1 << 30) / ((int64_t)a.n_pad * d * 4);
+    const int64_t fit = ((int64_t)4 << 30) / ((int64_t)a.n_pad * d * 4);
     a.pairs = (int)(fit < 1 ? 1 : fit < all_pairs ? fit : all_pairs);
   } else if (a.many_rows) {
     while (a.b.page_tokens % a.box_rows) a.box_rows /= 2;
   }
   a.cols = a.many_rows ? prompt_cols(d) : kCols;
   a.tile = a.many_rows ? kPromptTile : kKvBlock;
-  a.col_tiles = (int)(((int64_t)a.b.max_rows * a.G + a.cols - 1) / a.cols);
+  a.col_tiles = (int)((max_cols + a.cols - 1) / a.cols);
+  const int64_t dense = (int64_t)a.b.num_seqs * a.col_tiles;
+  const int64_t packed = (int64_t)a.b.num_rows * a.G / a.cols + a.b.num_seqs;
+  a.dense = a.b.q_start == nullptr || dense <= packed;
+  const int64_t units = a.dense ? dense : packed;
+  a.units = (int)(units < INT32_MAX ? units : INT32_MAX);  // (the caller checks the launch's size)
   // the most tiles that one unit's columns can see
   const int64_t tokens = (a.cols + a.G - 2) / a.G + 1;  // tokens that `cols` columns can span
   int64_t most = ((int64_t)a.b.max_len + a.tile - 1) / a.tile;
@@ -697,20 +708,20 @@ void plan_kv_attention(KvAttnParams &a, bool f8) {
     if (windowed) most = w;
   }
   if (most < 1) most = 1;
-  const int64_t base = (int64_t)a.b.num_seqs * a.b.h_kv * a.col_tiles;
+  const int64_t base = units * a.b.h_kv;
   int64_t splits;
   a.tail_from = 0;
   if (a.many_rows) {
-    // One block an SM.  Fewer units than SMs: each is divided.  More, of about equal
-    // length (a chunk over a long context, a window): those that would be left over
-    // for a last, partly filled wave are divided to fill it.  (Units of a prompt from
-    // its start grow with their rows; the short ones come last and fill the gaps.)
-    const int64_t units = (int64_t)a.pairs * a.col_tiles;
+    // One block an SM.  Fewer units than SMs: each is divided.  More, of one sequence
+    // and about equal length (a chunk over a long context, a window): those that
+    // would be left over for a last, partly filled wave are divided to fill it.
+    // (Units of a prompt from its start grow with their rows; the short ones come
+    // last and fill the gaps.)
     const bool even = windowed || (int64_t)a.b.max_len >= 4 * (int64_t)a.b.max_rows;
-    splits = 148 / units;
-    if (units > 148 && even && a.pairs == all_pairs && units % 148) {
-      a.tail_from = (int)(units - units % 148);
-      splits = 148 / (units % 148);
+    splits = 148 / base;
+    if (base > 148 && even && a.b.num_seqs == 1 && a.pairs == all_pairs && base % 148) {
+      a.tail_from = (int)(base - base % 148);
+      splits = 148 / (base % 148);
     }
     if (splits > most / 8) splits = most / 8;
   } else {
@@ -728,6 +739,33 @@ void plan_kv_attention(KvAttnParams &a, bool f8) {
   if (splits < 1) splits = 1;
   a.tiles_per_split = (int)((most + splits - 1) / splits);
   a.splits = (int)((most + a.tiles_per_split - 1) / a.tiles_per_split);
+}
+
+int plan_kv_attention(const KvAttnParams &a, bool f8, KvAttnParams (&plan)[2]) {
+  // The tcgen05 kernel multiplies 256 columns at a time (128 beyond 128 dimensions).
+  // It takes sequences of 64 columns or more, if the queries are bf16; its tensor
+  // map counts the cache's rows in 31 bits.
+  const int64_t rows = (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
+  const bool many = a.q_bf16 && a.d >= 64 && (int64_t)a.b.max_rows * a.G >= kManyCols &&
+                    a.G <= 4096 && (f8 || rows < ((int64_t)1 << 31));
+  plan[0] = a;
+  plan[0].many_rows = many;
+  plan[0].own = kEverySequence;
+  plan[0].report = 1;
+  // Sequences may have more rows or fewer (a prompt beside decoded tokens): those
+  // with few go to the few-rows kernel, which divides a long context among blocks
+  // and reads e4m3 as it is.
+  const bool both = many && a.b.q_start != nullptr && a.b.num_seqs > 1;
+  if (both) {
+    plan[1] = plan[0];
+    plan[0].own = kManyRows;
+    plan[1].own = kFewRows;
+    plan[1].many_rows = 0;
+    plan[1].report = 0;
+    plan_one(plan[1], f8);
+  }
+  plan_one(plan[0], f8);
+  return both ? 2 : 1;
 }
 
 cudaError_t launch_kv_attention(const KvAttnParams &a, bool f8, cudaStream_t s) {

@@ -13,6 +13,11 @@ namespace fathom {
 constexpr int prompt_cols(int d) { return d <= 128 ? 256 : 128; }
 constexpr int kPromptTile = 128;
 
+// From this many columns (rows times heads of a KV head) on a sequence goes to the
+// many-rows kernel.
+constexpr int kManyCols = 64;
+enum KvOwn { kEverySequence = 0, kFewRows = 1, kManyRows = 2 };
+
 struct KvAttnParams {
   KvBatch b;
   const void *ck, *cv;
@@ -30,18 +35,41 @@ struct KvAttnParams {
   // (token, head) pairs of one sequence and KV head; it goes through its keys in
   // tiles of `tile`, divided over `splits` thread blocks.
   int many_rows;  // the tcgen05 kernel
+  int own;        // 0: every sequence; kFewRows, kManyRows: those with fewer than
+                  // kManyCols columns, the others
+  int report;     // this launch writes the status
   int cols, tile;
-  int col_tiles, tiles_per_split, splits;
+  // Units of one KV head: `dense`, col_tiles for each sequence; else sequence s
+  // starts at unit q_start[s] G / cols + s (it needs no more than it has there).
+  int units, dense, col_tiles;
+  int tiles_per_split, splits;
   // many_rows: the (sequence, KV head) pairs of one launch; the units in order of
   // work from which on they are divided (the others are not); the rows of a K or V
   // box; e4m3: tokens of a pair in the widened copy (0: there is none)
   int pair0, pairs, tail_from, box_rows, n_pad;
   const uint16_t *wide;  // [2][pairs][n_pad][d] bf16
   WsStatus *status;
-  int *taint;       // many_rows: [units][splits], see kv_prompt.cu
+  int *taint;       // many_rows: [units * h_kv][splits], see kv_prompt.cu
   float2 *part_ml;  // [splits][num_rows * h_q]: maximum (log2 units), sum
   float *part_o;    // [splits][num_rows * h_q][d]
 };
+
+__device__ __forceinline__ bool owns(const KvAttnParams &a, const KvSeq &q) {
+  return a.own == kEverySequence || (q.rows * a.G >= kManyCols) == (a.own == kManyRows);
+}
+
+// Unit y of a KV head: its sequence and which of the sequence's units it is.
+struct KvUnit {
+  int s, ct;
+};
+
+__device__ __forceinline__ KvUnit kv_unit(const KvAttnParams &a, int y) {
+  if (a.dense) return {y / a.col_tiles, y % a.col_tiles};
+  auto base = [&](int i) { return (int64_t)a.b.q_start[i] * a.G / a.cols + i; };
+  const int s = find_seq(a.b.num_seqs, y, base);
+  const int64_t ct = y - base(s);
+  return {s, ct < 0 || ct >= a.col_tiles ? a.col_tiles : (int)ct};  // (col_tiles: none)
+}
 
 // Whether a row at position p sees token j.
 __device__ __forceinline__ bool sees(const KvAttnParams &a, int p, int j) {
@@ -105,7 +133,8 @@ __device__ __forceinline__ void write_status(const KvAttnParams &a) {
 
 // kv_attention.cu
 cudaError_t launch_kv_attention(const KvAttnParams &a, bool f8, cudaStream_t s);
-void plan_kv_attention(KvAttnParams &a, bool f8);
+// The launches of one call, one or two (long and short sequences apart), into plan.
+int plan_kv_attention(const KvAttnParams &a, bool f8, KvAttnParams (&plan)[2]);
 // kv_prompt.cu: the tcgen05 kernel, and the widening before it
 cudaError_t launch_kv_prompt(const KvAttnParams &a, bool f8, cudaStream_t s);
 

@@ -228,28 +228,21 @@ struct Columns {
   __device__ __forceinline__ int head_of(int x) const { return head + x - row_of(x) * G; }
 };
 
-// The units' order of work: later rows see more keys, so they come first.  Units
-// from number tail_from on are divided over `splits` blocks each.
+// A thread block's number among a launch's units (those of all KV heads side by
+// side) and their splits: units from number tail_from on are divided over `splits`
+// blocks each.
 struct Unit {
-  int split, splits, pair, rb;
+  int unit, split, splits;
 };
 
 __device__ __forceinline__ Unit unit_of(const KvAttnParams &a, int x) {
-  Unit u;
-  u.split = 0;
-  u.splits = 1;
-  if (x >= a.tail_from) {
-    u.split = (x - a.tail_from) % a.splits;
-    u.splits = a.splits;
-    x = a.tail_from + (x - a.tail_from) / a.splits;
-  }
-  u.pair = a.pair0 + x % a.pairs;
-  u.rb = a.col_tiles - 1 - x / a.pairs;
-  return u;
+  if (x < a.tail_from) return {x, 0, 1};
+  x -= a.tail_from;
+  return {a.tail_from + x / a.splits, x % a.splits, a.splits};
 }
 
 __host__ __device__ __forceinline__ int unit_blocks(const KvAttnParams &a) {
-  const int units = a.pairs * a.col_tiles, tail = units > a.tail_from ? units - a.tail_from : 0;
+  const int units = a.units * a.b.h_kv, tail = units > a.tail_from ? units - a.tail_from : 0;
   return units - tail + tail * a.splits;
 }
 
@@ -272,13 +265,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Unit u = unit_of(a, blockIdx.x);
-  const int split = u.split, rb = u.rb;
-  const int head = u.pair % a.b.h_kv, s = u.pair / a.b.h_kv;
-  int *taint = a.taint + ((int64_t)u.pair * a.col_tiles + rb) * a.splits + split;
+  const int split = u.split;
+  const int head = u.unit % a.b.h_kv;
+  const KvUnit ku = kv_unit(a, u.unit / a.b.h_kv);
+  const int s = ku.s, pair = s * a.b.h_kv + head;
+  if (pair < a.pair0 || pair >= a.pair0 + a.pairs) return;  // another launch's
+  int *taint = a.taint + (int64_t)u.unit * a.splits + split;
   if (tid < (u.splits == 1 ? a.splits : 1)) taint[tid] = 0;
   const KvSeq q = kv_seq(a.b, s);
+  // later rows see more keys: a sequence's last unit comes first
+  const int rb = (q.rows * a.G + kM * kTiles - 1) / (kM * kTiles) - 1 - ku.ct;
+  if (rb < 0 || !owns(a, q)) return;
   const int c0 = rb * kM * kTiles, c1 = min(c0 + kM * kTiles, q.rows * a.G);
-  if (c0 >= c1) return;
   const int first = q.len - q.rows;  // position of the sequence's first row
   const int p_lo = first + c0 / a.G, p_hi = first + (c1 - 1) / a.G;
   const KvTiles tiles = visible_tiles(a, p_lo, p_hi, kN);
@@ -357,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane >= kN / a.box_rows * panels || key > p_hi ||
         (last <= p_lo - a.window && key >= a.sinks))
       return -1;
-    if (a.n_pad > 0) return (u.pair - a.pair0) * a.n_pad + key;
+    if (a.n_pad > 0) return (pair - a.pair0) * a.n_pad + key;
     const int page = page_of(key);
     if (page < 0) return -1;
     return (page * a.b.h_kv + head) * a.b.page_tokens + key % a.b.page_tokens;
@@ -784,7 +782,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
   const int pair = blockIdx.x / per, key0 = blockIdx.x % per * kN;
   const int head = (a.pair0 + pair) % a.b.h_kv, s = (a.pair0 + pair) / a.b.h_kv;
   const KvSeq q = kv_seq(a.b, s);
-  if (q.rows == 0 || key0 >= q.len) return;
+  if (q.rows == 0 || key0 >= q.len || !owns(a, q)) return;
   const int from = q.len - q.rows - a.window;  // the last key before every row's window
   if (key0 + kN - 1 <= from && key0 >= a.sinks) return;
   for (int i = threadIdx.x; i < kN * pieces; i += kWidenThreads) {
@@ -861,7 +859,7 @@ cudaError_t launch(KvAttnParams a, bool f8, cudaStream_t s) {
                            static_cast<uint16_t *>(const_cast<void *>(v)));
     if (e == cudaSuccess)
       e = launch_dependent(kv_prompt_kernel<DP, FULL>,
-                           dim3((unsigned)(unit_blocks(a) + (a.pair0 == 0))),
+                           dim3((unsigned)(unit_blocks(a) + (a.pair0 == 0 ? a.report : 0))),
                            dim3(kThreads), smem, s, a, map_k, map_v);
   }
   return e;

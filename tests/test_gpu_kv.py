@@ -330,6 +330,43 @@ def test_attention_many_rows(d, G, page, lens, rows, window, sinks, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,rows,window", [
+    ([700, 33, 1200, 5, 90, 64], [1, 1, 200, 5, 90, 16], 0), ([40, 800, 41], [15, 300, 1], 70),
+    ([3000, 20, 20, 20, 20], [1, 15, 16, 17, 0], 0)])
+def test_attention_prompts_beside_decoded_tokens(lens, rows, window, qt, dtype):
+    """Long and short sequences in one batch: each goes to the kernel for its rows, a few
+    on either side of where that changes (16 rows of 4 heads)."""
+    rng = np.random.default_rng(21)
+    ct, qt = BF16 if dtype == "bf16" else F8, BF16 if qt == "bf16" else F32
+    cache = make_cache(rng, 70, 64, 2, 128, ct)
+    batch, table, seqs = make_batch(rng, 70, 64, lens, rows, num_rows=sum(rows) + 3)
+    q = randn(rng, batch.num_rows, 8, 128, dtype=qt)
+    out, lse = torch.full_like(q, 7.0), torch.full((batch.num_rows, 8), 7.0, device="cuda")
+    F.kv_attention(cache, batch, q, window=window, sinks=3, out=out, lse=lse)
+    torch.cuda.synchronize()
+    want = R.attention(ref_cache(cache), table, seqs, R.f64(q), 1 / math.sqrt(128), window, 3, WEIGHT[ct, qt],
+                       R.half_step(qt))
+    check_attention((out, lse), want)
+    assert (out[-3:] == 7.0).all() and (lse[-3:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attention_many_heads_of_one_kv_head(dtype):
+    """64 and more query heads a KV head: one decoded token fills a many-rows unit."""
+    rng = np.random.default_rng(22)
+    ct = BF16 if dtype == "bf16" else F8
+    for G, lens in ((64, [900, 3]), (130, [200])):
+        cache = make_cache(rng, 20, 64, 1, 64, ct)
+        batch, table, seqs = make_batch(rng, 20, 64, lens)
+        q = randn(rng, len(lens), G, 64)
+        got = F.kv_attention(cache, batch, q)
+        torch.cuda.synchronize()
+        want = R.attention(ref_cache(cache), table, seqs, R.f64(q), 1 / 8, weight_step=WEIGHT[ct, BF16])
+        check_attention(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (500, 20), (3000, 0), (5000, 100)])
 def test_attention_split_over_blocks(dtype, window, sinks):
     """A context long enough that several blocks share it, with max_len far above

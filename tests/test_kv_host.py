@@ -113,7 +113,8 @@ def test_null_and_host_pointers_are_refused(L):
 
 def test_nothing_to_do_is_ok(L):
     for batch in (_batch(num_seqs=0, num_rows=0, max_rows=0), _batch(num_seqs=0, num_rows=0, max_rows=0,
-                                                                   max_len=0, table_width=0)):
+                                                                   max_len=0, table_width=0),
+                  _batch(q_start=16, num_rows=9, max_rows=0)):
         assert L.fathom_kv_append(ctypes.byref(_app(batch=batch)), None) == F.OK
         assert L.fathom_kv_attention(ctypes.byref(_attn(batch=batch)), None, 0, None) == F.OK
 
