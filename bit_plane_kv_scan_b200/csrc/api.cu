@@ -297,12 +297,10 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
                 a->batch.max_rows, p.G);
   plans = plan_kv_attention(p, a->cache.dtype == FATHOM_E4M3, plan);
   for (int i = 0; i < plans; ++i)
-    if ((double)plan[i].units * p.b.h_kv * plan[i].splits >= 2147483647.0)
+    if ((double)plan[i].units * p.b.h_kv * (plan[i].splits > 64 ? plan[i].splits : 64) >= 2147483647.0)
       return fail(FATHOM_ERR_UNSUPPORTED,
                   "num_seqs=%d max_rows=%d h_q=%d: too many blocks for one launch", p.b.num_seqs,
                   p.b.max_rows, p.h_q);
-  if ((double)p.b.num_rows * p.h_q >= 2147483647.0)
-    return fail(FATHOM_ERR_UNSUPPORTED, "num_rows=%d times h_q=%d is too many", p.b.num_rows, p.h_q);
   return FATHOM_OK;
 }
 

@@ -532,38 +532,24 @@ __global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
   }
 }
 
-// Joins the splits of one (row, head): a block each, its warps every fourth split.
-// The splits' maxima and sums are read 32 at a time, their outputs 8 at a time, so
-// that their latency is not paid split by split.
+// One warp's part in joining the splits of one (row, head): of n splits those from
+// `from` on, every `step`-th; lane l has dimensions l, l + 32, ...  The splits' maxima
+// and sums are read 32 at a time, their outputs 8 at a time, so that their latency
+// is not paid split by split.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, float shift) {
-  grid_dependency_wait();
-  allow_dependent_launch();
+__device__ __forceinline__ void join_splits(const KvAttnParams &a, int64_t rh, int n, int from,
+                                            int step, float &m, float &l, float (&o)[D / 32]) {
   constexpr int kPer = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t rh = blockIdx.x;
-  const int row = (int)(rh / a.h_q), h = (int)(rh % a.h_q);
-  const int s = a.b.q_start ? find_seq(a.b.num_seqs, row, [&](int i) { return a.b.q_start[i]; }) : row;
-  const KvSeq q = kv_seq(a.b, s);
-  if (row < q.row0 || row >= q.row0 + q.rows || !owns(a, q)) return;
-  const int col = (row - q.row0) * a.G + h % a.G, c0 = col / a.cols * a.cols;
-  // (many rows of one sequence: the unit's number in order of work; those before
-  // tail_from are whole)
-  if (a.tail_from > 0 &&
-      ((q.rows * a.G - 1) / a.cols - col / a.cols) * a.b.h_kv + h / a.G < a.tail_from)
-    return;
-  const int c1 = min(c0 + a.cols, q.rows * a.G), first = q.len - q.rows;
-  const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
-  const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
-  const int64_t step = (int64_t)a.b.num_rows * a.h_q;
-  const int mine = n > warp ? (n - warp + kWarps - 1) / kWarps : 0;
-  float m = -INFINITY, l = 0.0f, o[kPer];
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)a.b.num_rows * a.h_q;
+  const int mine = n > from ? (n - from + step - 1) / step : 0;
+  m = -INFINITY;
+  l = 0.0f;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) o[j] = 0.0f;
   for (int i0 = 0; i0 < mine; i0 += 32) {
-    const int split = warp + kWarps * (i0 + lane);
-    const float2 ml = split < n ? a.part_ml[split * step + rh] : make_float2(-INFINITY, 0.0f);
+    const int split = from + step * (i0 + lane);
+    const float2 ml = split < n ? a.part_ml[split * rows + rh] : make_float2(-INFINITY, 0.0f);
     float big = ml.x;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
@@ -583,7 +569,7 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, fl
       float v[8][kPer];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float *po = a.part_o + ((warp + kWarps * (int64_t)(i0 + k0 + k)) * step + rh) * D + lane;
+        const float *po = a.part_o + ((from + step * (int64_t)(i0 + k0 + k)) * rows + rh) * D + lane;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[k][j] = k0 + k < here ? po[32 * j] : 0.0f;
       }
@@ -596,12 +582,34 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, fl
       }
     }
   }
+}
+
+// Few rows: a block joins the splits of one column of a unit, its warps every
+// fourth.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttnParams a, float shift) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = (int)(blockIdx.x / kCols), head = x % a.b.h_kv;
+  const KvUnit u = kv_unit(a, x / a.b.h_kv);
+  const KvSeq q = kv_seq(a.b, u.s);
+  const int c1 = (int)min((int64_t)(u.ct + 1) * kCols, (int64_t)q.rows * a.G), c0 = u.ct * kCols;
+  const int col = c0 + (int)(blockIdx.x % kCols);
+  if (col >= c1 || !owns(a, q)) return;
+  const int first = q.len - q.rows;
+  const int64_t rh = (int64_t)(q.row0 + col / a.G) * a.h_q + head * a.G + col % a.G;
+  const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
+  const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
+  float m, l, o[D / 32];
+  join_splits<D>(a, rh, n, warp, kWarps, m, l, o);
   if (lane == 0) {
     s_m[warp] = m;
     s_l[warp] = l;
   }
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) s_o[warp][32 * j + lane] = o[j];
+  for (int j = 0; j < D / 32; ++j) s_o[warp][32 * j + lane] = o[j];
   __syncthreads();
   for (int c = threadIdx.x; c < D; c += kThreads) {
     float M = -INFINITY, L = 0.0f, O = 0.0f;
@@ -616,6 +624,31 @@ __global__ void __launch_bounds__(kThreads) kv_combine_kernel(KvAttnParams a, fl
     store_out(a, rh * D + c, L > 0.0f ? O / L : (L == 0.0f ? 0.0f : L));
     if (c == 0 && a.lse) a.lse[rh] = lse_of(M, L, shift);
   }
+}
+
+// Many rows: a warp joins the splits of one column of a divided unit.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_join_units_kernel(KvAttnParams a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int per = a.cols / kWarps, lane = threadIdx.x & 31;  // blocks of a unit
+  const int x = a.tail_from + (int)blockIdx.x / per, head = x % a.b.h_kv;
+  const KvUnit u = kv_unit(a, x / a.b.h_kv);
+  const KvSeq q = kv_seq(a.b, u.s);
+  const int rb = (q.rows * a.G + a.cols - 1) / a.cols - 1 - u.ct;  // (units come last first)
+  if (rb < 0 || !owns(a, q)) return;
+  const int c0 = rb * a.cols, c1 = min(c0 + a.cols, q.rows * a.G), first = q.len - q.rows;
+  const int col = c0 + (int)blockIdx.x % per * kWarps + (threadIdx.x >> 5);
+  if (col >= c1) return;
+  const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
+  const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
+  const int64_t rh = (int64_t)(q.row0 + col / a.G) * a.h_q + head * a.G + col % a.G;
+  float m, l, o[D / 32];
+  join_splits<D>(a, rh, n, 0, 1, m, l, o);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+    store_out(a, rh * D + 32 * j + lane, l > 0.0f ? o[j] / l : (l == 0.0f ? 0.0f : l));
+  if (lane == 0 && a.lse) a.lse[rh] = lse_of(m, l, 0.0f);
 }
 
 template <int D, bool F8, typename Kernel>
@@ -648,11 +681,14 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
   else
     e = a.q_bf16 ? launch_ring<D, false>(kv_attention_kernel<D, false, 1>, blocks, a, s)
                  : launch_ring<D, false>(kv_attention_kernel<D, false, 3>, blocks, a, s);
-  if (e == cudaSuccess && a.splits > 1) {
-    const int64_t rh = (int64_t)a.b.num_rows * a.h_q;
-    e = launch_dependent(kv_combine_kernel<D>, dim3((unsigned)rh), block, 0, s, a,
-                         f8 && !a.many_rows ? 15.0f : 0.0f);
-  }
+  if (e == cudaSuccess && a.splits > 1 && !a.many_rows)
+    e = launch_dependent(kv_join_kernel<D>, dim3((unsigned)((int64_t)a.units * a.b.h_kv * kCols)),
+                         block, 0, s, a, f8 ? 15.0f : 0.0f);
+  if constexpr (D >= 64)
+    if (e == cudaSuccess && a.splits > 1 && a.many_rows) {
+      const int64_t n = ((int64_t)a.units * a.b.h_kv - a.tail_from) * (a.cols / kWarps);
+      e = launch_dependent(kv_join_units_kernel<D>, dim3((unsigned)n), block, 0, s, a);
+    }
   if constexpr (D >= 64)
     if (e == cudaSuccess && a.many_rows)
       e = f8 ? launch_redo<D, true>(a, s) : launch_redo<D, false>(a, s);
