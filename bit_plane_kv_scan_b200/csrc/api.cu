@@ -311,7 +311,8 @@ size_t kv_workspace(KvAttnParams (&plan)[2], int plans, unsigned char *base) {
   size_t at = sizeof(WsStatus);
   for (int i = 0; i < plans; ++i) {
     KvAttnParams &p = plan[i];
-    const size_t parts = p.splits > 1 ? (size_t)p.splits * p.b.num_rows * p.h_q : 0;
+    const size_t parts =
+        p.splits > 1 && !p.cluster ? (size_t)p.splits * p.b.num_rows * p.h_q : 0;
     const size_t marks = p.many_rows ? (size_t)p.units * p.b.h_kv * p.splits : 0;
     if (base) {
       p.status = reinterpret_cast<WsStatus *>(base);

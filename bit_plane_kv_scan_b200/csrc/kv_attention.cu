@@ -19,11 +19,12 @@
 //     pieces g of every eight; byte permutes pair two keys' elements.
 //     P^T comes from S^T by movmatrix.
 // Each warp takes every fourth 16-key tile of its block's run of tiles, through a
-// ring of its own in shared memory that 16-byte asynchronous copies fill 2 to 5
+// ring of its own in shared memory that 16-byte asynchronous copies fill 1 or 2
 // tiles ahead (no barrier between warps); its lanes look up the pages and scales
 // of 32 tiles at once, a batch ahead.  The four warps' results meet in shared
-// memory; where a sequence's tiles are split over several blocks, a second kernel
-// joins the blocks' results (maximum, sum, output).
+// memory; where a sequence's tiles are split over several blocks, these join their
+// results (maximum, sum, output) through the shared memory of a cluster, or, more
+// than 16, through the workspace and a second kernel.
 //
 // E4M3: codes become fp16 exactly (the hardware's conversion).  q is scaled to
 // fp16 by a power of two per row and head; a 16-key tile is one scale block, so
@@ -36,10 +37,13 @@
 // Masks: only tiles at the edge of what some column sees are masked.  There a V
 // row that a token does not see is replaced by zeros for that token, so that
 // what it holds (0 * NaN) cannot reach it.
+#include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
 #include "kv_attention.cuh"
 #include "tc_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace fathom {
 
@@ -48,6 +52,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCols = 8;  // (token, head) pairs of a block: the MMA's n
+constexpr int kMaxCluster = 16;
 
 template <bool F8>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -120,6 +125,10 @@ __device__ __forceinline__ void load_bytes(uint32_t p, uint32_t *w) {
   }
 }
 
+// Tiles of a warp's ring.  A row of 256 bytes: 2, so that three blocks fit on an SM
+// (64 windowed bf16 sessions: 162 us, against 172 with 3 tiles and two blocks).
+constexpr int ring_depth(int row_bytes) { return row_bytes == 256 ? 2 : 3; }
+
 template <int D, bool F8>
 struct Shape {
   static constexpr int kRow = F8 ? D : 2 * D;                    // bytes of a row
@@ -131,7 +140,7 @@ struct Shape {
   // (an odd number of 16-byte pieces: the pieces that 8 lanes read at once lie
   // in different banks).
   static constexpr int kPitch = kRow + 16, kSide = kKvBlock * kPitch, kStage = 2 * kSide;
-  static constexpr int kDepth = 3;
+  static constexpr int kDepth = ring_depth(kRow);
   static constexpr int kSmem = kWarps * kDepth * kStage;
   // The byte of piece j of the lane's part of a K row: two neighbouring pieces of
   // 128 bytes, so that four lanes' pieces 0 are every second one.
@@ -202,7 +211,10 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
   extern __shared__ __align__(16) unsigned char s_ring[];
   // the warps' outputs meet where the rings were
   float(*s_o)[kCols][D + 4] = reinterpret_cast<float(*)[kCols][D + 4]>(s_ring);
-  static_assert(sizeof(float) * kWarps * kCols * (D + 4) <= S::kSmem, "outputs fit in the rings");
+  // and, of a cluster, this block's result behind them
+  float(*s_joined)[D] = reinterpret_cast<float(*)[D]>(s_ring + sizeof(float) * kWarps * kCols * (D + 4));
+  __shared__ float2 s_ml[kCols];
+  static_assert(sizeof(float) * kCols * (kWarps * (D + 4) + D) <= S::kSmem, "they fit in the rings");
   const KvSeq q = kv_seq(a.b, s);
   // columns of this block (ct may be past the sequence's last)
   const int c1 = (int)min((int64_t)(ct + 1) * kCols, (int64_t)q.rows * a.G), c0 = ct * kCols;
@@ -211,7 +223,7 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
   const int p_lo = first + c0 / a.G, p_hi = first + (c1 - 1) / a.G;
   const KvTiles tiles = visible_tiles(a, p_lo, p_hi, kKvBlock);
   const int i0 = split * a.tiles_per_split, i1 = min(i0 + a.tiles_per_split, tiles.count);
-  if (split > 0 && i0 >= tiles.count) return;
+  if (split > 0 && i0 >= tiles.count && !a.cluster) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   // this warp's tiles: number n is tile i0 + warp + kWarps n
@@ -473,6 +485,11 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
       // (a warp that saw nothing has zeros)
       O = fmaf(s_o[w][c][dim], f, O);
     }
+    if (a.cluster) {
+      s_joined[c][dim] = O;
+      if (dim == 0) s_ml[c] = make_float2(M, L);
+      continue;
+    }
     const int row = q.row0 + (c0 + c) / a.G, h = head * a.G + (c0 + c) % a.G;
     const int64_t rh = (int64_t)row * a.h_q + h;
     if (a.splits == 1) {
@@ -484,16 +501,37 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
       if (dim == 0) a.part_ml[part] = make_float2(M, L);
     }
   }
+  if (!a.cluster) return;
+  // the splits of a unit are a cluster: each block joins its share of the columns'
+  // dimensions over all of them
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();  // every block's result is in its shared memory
+  for (int y = split * kThreads + threadIdx.x; y < (c1 - c0) * D; y += a.splits * kThreads) {
+    const int c = y / D, dim = y % D;
+    float M = -INFINITY;
+    for (int r = 0; r < a.splits; ++r) M = fmaxf(M, cluster.map_shared_rank(&s_ml[c], r)->x);
+    float L = 0.0f, O = 0.0f;
+    for (int r = 0; r < a.splits; ++r) {
+      const float2 ml = *cluster.map_shared_rank(&s_ml[c], r);
+      const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : exp2f(ml.x - M);
+      L = fmaf(ml.y, f, L);
+      O = fmaf(*cluster.map_shared_rank(&s_joined[c][dim], r), f, O);
+    }
+    const int64_t rh = (int64_t)(q.row0 + (c0 + c) / a.G) * a.h_q + head * a.G + (c0 + c) % a.G;
+    store_out(a, rh * D + dim, L > 0.0f ? O / L : (L == 0.0f ? 0.0f : L));
+    if (dim == 0 && a.lse) a.lse[rh] = lse_of(M, L, kShift);
+  }
+  cluster.sync();  // the others have read this block's
 }
 
 template <int D, bool F8, int TERMS>
-__global__ void __launch_bounds__(kThreads, F8 && TERMS == 1 && D <= 128 ? 4 : 1)
+__global__ void __launch_bounds__(kThreads, TERMS > 1 || D > 128 ? 1 : F8 ? 4 : 3)
     kv_attention_kernel(KvAttnParams a) {
   grid_dependency_wait();
   allow_dependent_launch();
   int x = blockIdx.x;
-  if (x == a.units * a.b.h_kv * a.splits) {  // one more, if it reports
-    write_status(a);
+  if (x >= a.units * a.b.h_kv * a.splits) {  // one (cluster) more, if it reports
+    if (x == a.units * a.b.h_kv * a.splits) write_status(a);
     return;
   }
   const int split = x % a.splits;
@@ -511,6 +549,7 @@ __global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
   const int per = a.cols / kCols, units = a.units * a.b.h_kv;
   KvAttnParams b = a;
   b.splits = 1;
+  b.cluster = 0;
   b.tiles_per_split = 1 << 30;
   for (int x0 = blockIdx.x * kThreads; x0 < units; x0 += gridDim.x * kThreads) {
     // a thread looks at one unit's marks; marked ones are rare
@@ -654,23 +693,42 @@ __global__ void __launch_bounds__(kThreads) kv_join_units_kernel(KvAttnParams a)
 template <int D, bool F8, typename Kernel>
 cudaError_t launch_ring(Kernel kernel, int64_t blocks, const KvAttnParams &a, cudaStream_t s) {
   constexpr int smem = Shape<D, F8>::kSmem;
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, s, a);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && a.cluster && a.splits > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  if (!a.cluster) return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, s, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <int D, bool F8>
 cudaError_t launch_redo(const KvAttnParams &a, cudaStream_t s) {
   const int64_t blocks = ((int64_t)a.units * a.b.h_kv + kThreads - 1) / kThreads;
-  return launch_ring<D, F8>(kv_redo_kernel<D, F8>, blocks < 296 ? blocks : 296, a, s);
+  KvAttnParams b = a;
+  b.cluster = 0;
+  return launch_ring<D, F8>(kv_redo_kernel<D, F8>, blocks < 296 ? blocks : 296, b, s);
 }
 
 template <int D>
 cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
-  const int64_t blocks = (int64_t)a.units * a.b.h_kv * a.splits + a.report;
+  const int64_t blocks =
+      (int64_t)a.units * a.b.h_kv * a.splits + (a.report ? (a.cluster ? a.splits : 1) : 0);
   const dim3 block(kThreads);
   cudaError_t e;
   if (a.many_rows)
@@ -681,7 +739,7 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
   else
     e = a.q_bf16 ? launch_ring<D, false>(kv_attention_kernel<D, false, 1>, blocks, a, s)
                  : launch_ring<D, false>(kv_attention_kernel<D, false, 3>, blocks, a, s);
-  if (e == cudaSuccess && a.splits > 1 && !a.many_rows)
+  if (e == cudaSuccess && a.splits > 1 && !a.many_rows && !a.cluster)
     e = launch_dependent(kv_join_kernel<D>, dim3((unsigned)((int64_t)a.units * a.b.h_kv * kCols)),
                          block, 0, s, a, f8 ? 15.0f : 0.0f);
   if constexpr (D >= 64)
@@ -701,7 +759,7 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
 // (228 KB an SM, 1 KB of it for each block).
 static int kv_resident_blocks(int d, bool f8) {
   const int row = f8 ? d : 2 * d;
-  const int smem = kWarps * 3 * 2 * kKvBlock * (row + 16) + 1280;
+  const int smem = kWarps * ring_depth(row) * 2 * kKvBlock * (row + 16) + 1280;
   const int per = 228 * 1024 / smem;
   return 148 * (per > 4 ? 4 : per);
 }
@@ -775,6 +833,9 @@ static void plan_one(KvAttnParams &a, bool f8) {
   if (splits < 1) splits = 1;
   a.tiles_per_split = (int)((most + splits - 1) / splits);
   a.splits = (int)((most + a.tiles_per_split - 1) / a.tiles_per_split);
+  // Few splits are a cluster and join through its shared memory, without the
+  // workspace and a second launch.
+  a.cluster = !a.many_rows && a.splits > 1 && a.splits <= kMaxCluster;
 }
 
 int plan_kv_attention(const KvAttnParams &a, bool f8, KvAttnParams (&plan)[2]) {

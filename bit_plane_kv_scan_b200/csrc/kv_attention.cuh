@@ -43,6 +43,7 @@ struct KvAttnParams {
   // starts at unit q_start[s] G / cols + s (it needs no more than it has there).
   int units, dense, col_tiles;
   int tiles_per_split, splits;
+  int cluster;  // few rows: a unit's splits are a cluster
   // many_rows: the (sequence, KV head) pairs of one launch; the units in order of
   // work from which on they are divided (the others are not); the rows of a K or V
   // box; e4m3: tokens of a pair in the widened copy (0: there is none)
