@@ -438,7 +438,7 @@ FATHOM_API fathom_status fathom_sparse_attention(const fathom_attention_args *ar
  * page_table[s][j / page_tokens].  A page that is a whole context
  * (num_pages = 1, FATHOM_BF16) is the [h_kv][n][d] layout which
  * fathom_sparse_attention gathers from.
- * Requires d as FATHOM_MAX_D, page_tokens a positive multiple of
+ * Requires d as FATHOM_MAX_D, h_kv <= 65535, page_tokens a positive multiple of
  * FATHOM_KV_BLOCK up to 2^30, num_pages >= 1 and h_kv >= 1.
  */
 #define FATHOM_KV_BLOCK 16
@@ -538,12 +538,14 @@ FATHOM_API fathom_status fathom_kv_append(const fathom_kv_append_args *args, voi
  *        Rows that no sequence has are left as they were.
  * Products run on the tensor cores with sums, maxima and softmax statistics in
  * fp32.  FATHOM_BF16 queries: softmax weights are rounded to 16 bits before they
- * meet V.  FATHOM_F32 queries and their weights are split into 16-bit terms
- * that keep 22 bits or more.
+ * meet V (bf16; fp16 where few rows read an FATHOM_E4M3 cache).  FATHOM_F32
+ * queries and their weights are split into 16-bit terms that keep 22 bits or more.
  * Requires h_q a multiple of h_kv, a finite softmax_scale, window >= 0 and
  * sinks >= 0.  The workspace (fathom_kv_attention_workspace_size bytes, 0 on
  * bad arguments) is 256-byte aligned device memory, which the call need not
- * find cleared; calls sharing one must not overlap.  It starts with the status
+ * find cleared; calls sharing one must not overlap.  (Many rows over an
+ * FATHOM_E4M3 cache need up to 4 GiB of it, for the keys and values widened to
+ * bf16, or one KV head of one sequence where that is more.)  It starts with the status
  * that fathom_check_device_status reads: a sequence that the batch's bounds
  * reject is a device fault.
  */
