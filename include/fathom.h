@@ -438,8 +438,8 @@ FATHOM_API fathom_status fathom_sparse_attention(const fathom_attention_args *ar
  * page_table[s][j / page_tokens].  A page that is a whole context
  * (num_pages = 1, FATHOM_BF16) is the [h_kv][n][d] layout which
  * fathom_sparse_attention gathers from.
- * Requires d as FATHOM_MAX_D, h_kv <= 65535, page_tokens a positive multiple of
- * FATHOM_KV_BLOCK up to 2^30, num_pages >= 1 and h_kv >= 1.
+ * Requires d as FATHOM_MAX_D, 1 <= h_kv <= 65535, page_tokens a positive multiple of
+ * FATHOM_KV_BLOCK up to 2^30 and num_pages >= 1.
  */
 #define FATHOM_KV_BLOCK 16
 #define FATHOM_KV_SCALE_MIN 8
@@ -475,7 +475,7 @@ typedef struct fathom_kv_batch {
   const int32_t *seq_len;
   const int32_t *q_start;
   int num_seqs, table_width, num_rows, max_rows;
-  int64_t max_len;  /* 0 <= max_len <= FATHOM_KV_MAX_LEN */
+  int64_t max_len;  /* 0 <= max_len <= FATHOM_KV_MAX_LEN; num_seqs <= 2^24, num_rows <= 2^30 */
 } fathom_kv_batch;
 
 /* fathom_kv_append -- puts the rows' keys and values into the cache, keys (and

@@ -32,7 +32,7 @@ def _lib():
     yield
 
 
-def make_cache(rng, pages, page, h_kv, d, dtype, fill=True):
+def make_cache(rng, pages, page, h_kv, d, dtype):
     """A cache of random values (every page, so that strays show)."""
     if dtype == BF16:
         k, v = (torch.from_numpy(rng.normal(size=(pages, h_kv, page, d)).astype(np.float32)).to(BF16)
@@ -676,3 +676,71 @@ def test_one_page_cache_feeds_the_sparse_attention():
                        WEIGHT[BF16, F32], R.half_step(F32))
     check_attention((o2, l2), want)
     check_attention((o[None], l[None]), want)  # fp32 throughout: within the same bounds
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 96, 160, 256])
+def test_units_with_an_unseen_nan_are_done_again(d, dtype):
+    """Many rows at the other widths: a NaN token among the rows' own, seen by the later ones
+    alone."""
+    rng = np.random.default_rng(23)
+    ct = BF16 if dtype == "bf16" else F8
+    n, m, bad = 300, 170, 222
+    cache = make_cache(rng, 6, 64, 2, d, ct)
+    batch, table, seqs = make_batch(rng, 6, 64, [n], [m])
+    q = randn(rng, m, 4, d)
+    ref = list(R.attention(ref_cache(cache), table, seqs, R.f64(q), 1 / math.sqrt(d), weight_step=WEIGHT[ct, BF16]))
+    at = (table[0][bad // 64], 1, bad % 64)  # of KV head 1: query heads 2 and 3
+    if ct == BF16:
+        cache.v[at] = math.nan
+    else:
+        cache.v.view(torch.uint8)[at] = 0x7f
+    got = F.kv_attention(cache, batch, q)
+    torch.cuda.synchronize()
+    late = slice(bad - (n - m), None)
+    assert torch.isnan(got[0][late, 2:]).all() and torch.isfinite(got[0][late, :2]).all()
+    ref[1][late, 2:] = np.nan  # compare the others
+    check_attention(got, ref)
+
+
+def test_calls_on_two_streams_at_once():
+    """Prompts and decoded tokens on two streams without order between them: each call has
+    a workspace of its own."""
+    rng = np.random.default_rng(24)
+    jobs = []
+    for ct, lens, rows in ((BF16, [1500, 40], [600, 1]), (F8, [1500, 40], [600, 1]), (F8, [3000, 2000], None),
+                           (BF16, [9000], None)):
+        pages = sum(-(-x // 64) for x in lens)
+        cache = make_cache(rng, pages, 64, 2, 128, ct)
+        batch, _, _ = make_batch(rng, pages, 64, lens, rows)
+        q = randn(rng, batch.num_rows, 8, 128)
+        jobs.append((cache, batch, q, F.kv_attention(cache, batch, q)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(12):
+        for s, k in zip(streams, (i, i + 1)):
+            cache, batch, q, want = jobs[k % len(jobs)]
+            got.append((F.kv_attention(cache, batch, q, stream=s), want))
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in got:
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_sequences_that_share_pages(dtype):
+    """A prefix's pages in two sequences' tables, and one page twice in a table, for
+    reading."""
+    rng = np.random.default_rng(25)
+    ct = BF16 if dtype == "bf16" else F8
+    cache = make_cache(rng, 5, 32, 1, 64, ct)
+    table = np.array([[0, 1, 2], [0, 1, 3], [4, 4, 0]], dtype=np.int32)
+    lens, rows = [90, 80, 96], [20, 1, 40]
+    start = np.array([0, 20, 21, 61], dtype=np.int32)
+    batch = F.KVBatch(torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                      torch.from_numpy(start).cuda(), num_rows=61, max_rows=40)
+    q = randn(rng, 61, 4, 64)
+    got = F.kv_attention(cache, batch, q)
+    torch.cuda.synchronize()
+    want = R.attention(ref_cache(cache), table, R.sequences(lens, start), R.f64(q), 1 / 8, weight_step=WEIGHT[ct, BF16])
+    check_attention(got, want)
