@@ -744,3 +744,60 @@ def test_sequences_that_share_pages(dtype):
     torch.cuda.synchronize()
     want = R.attention(ref_cache(cache), table, R.sequences(lens, start), R.f64(q), 1 / 8, weight_step=WEIGHT[ct, BF16])
     check_attention(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_captured_prompt_chunks_with_one_workspace(dtype):
+    """Chunks of two prompts captured on two caches with one workspace between them, replayed
+    as the sequences grow, each equal to eager calls with workspaces of their own."""
+    rng = np.random.default_rng(26)
+    ct = BF16 if dtype == "bf16" else F8
+    rows, d = [200, 131], 128
+    caches = [make_cache(rng, 128, 64, 2, d, ct) for _ in range(2)]
+    table = torch.from_numpy(rng.permutation(128).reshape(2, 64).astype(np.int32)).cuda()
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+    batch = F.KVBatch(table, n, torch.tensor([0, 200, 331], dtype=torch.int32).cuda(), num_rows=331,
+                      max_rows=200, max_len=4096)
+    q = randn(rng, 331, 8, d)
+    n += torch.tensor(rows, dtype=torch.int32, device="cuda")
+    ws = F.Workspace()
+    for c in caches:  # the workspace grows before the capture
+        F.kv_attention(c, batch, q, workspace=ws)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in caches:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(F.kv_attention(c, batch, q, workspace=ws))
+        graphs.append(g)
+    for lens in ([200, 131], [201, 1000], [4096, 140], [3000, 0], [777, 4001]):
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.copy_(randn(rng, *q.shape))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        got = [(o.clone(), l.clone()) for o, l in outs]
+        for c, (o, l) in zip(caches, got):
+            o2, l2 = F.kv_attention(c, batch, q)
+            torch.cuda.synchronize()
+            assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("m", [1, 3, 90])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_query_that_is_not_finite_spoils_its_own_row(bad, dtype, m):
+    """One element of one row's head: that row's head alone may change."""
+    rng = np.random.default_rng(27)
+    cache = make_cache(rng, 8, 64, 1, 128, BF16 if dtype == "bf16" else F8)
+    batch, _, _ = make_batch(rng, 8, 64, [500], [m])
+    q = randn(rng, m, 4, 128)
+    want = F.kv_attention(cache, batch, q)
+    q2 = q.clone()
+    q2[m // 2, 1, 77] = bad
+    got = F.kv_attention(cache, batch, q2)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[0][m // 2, 1]).all()
+    for a, b in zip(got, want):
+        a[m // 2, 1], b[m // 2, 1] = 0, 0
+        assert torch.equal(a, b)
