@@ -17,7 +17,11 @@
 // comes from the elements before the rotation, which makes it the same whatever
 // the sines' last bit, and leaves room for sqrt 2.
 //
-// Bound by bytes: every element is read and written once.
+// Bound by bytes: every element is read and written once.  With 32 query and 8 KV
+// heads, d = 128: 8192 rows into bf16 pages 42 us (73% of the copy rate), prompts of
+// 5003 to 16384 rows into e4m3 pages 160 us (62%), a decoded row 3 us.  A thread has
+// one task of 32 bytes on its way; two ahead (177 us) or prefetches into L2 (171)
+// are no faster.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

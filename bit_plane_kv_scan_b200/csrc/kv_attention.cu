@@ -34,6 +34,11 @@
 // fp32 queries: q and the weights are split into 2 (fp16) or 3 (bf16) terms and
 // the products run once for each.
 //
+// With 32 query and 8 KV heads, d = 128: a row over 1M e4m3 tokens 377 to 402 us by
+// board (82 to 87% of the copy rate; the board's power is the limit), 64 rows of
+// windows of 4096 bf16 tokens 160 us (84%), a row over 4099 tokens 11 us.  e4m3 MMAs
+// for S, q split into two terms, draw more power: 416 us against 391 in a loop.
+//
 // Masks: only tiles at the edge of what some column sees are masked.  There a V
 // row that a token does not see is replaced by zeros for that token, so that
 // what it holds (0 * NaN) cannot reach it.

@@ -28,6 +28,10 @@
 // the units, each for itself, held them to 528 TFLOP/s; loads by cp.async from
 // four warps held bf16 to 807.)
 //
+// With 32 query and 8 KV heads, d = 128: 4096 rows over 32768 e4m3 tokens 1.78 ms
+// (1160 TFLOP/s, at the board's power limit), 8192 rows with a window of 2048 over
+// bf16 309 us (780 TFLOP/s: a unit's 18 tiles of keys do not hide its start and end).
+//
 // Masks are applied to S, where a tile of keys is not seen whole.  A masked key's
 // weight is an exact zero, but 0 * NaN is not.  So in such tiles V's rows that no
 // row of the unit sees become zeros, and where a value that some row does not see
