@@ -773,7 +773,7 @@ static int kv_resident_blocks(int d, bool f8) {
 static void plan_one(KvAttnParams &a, bool f8) {
   const int d = a.d;
   int64_t max_cols = (int64_t)a.b.max_rows * a.G;
-  if (a.own == kFewRows && max_cols >= kManyCols) max_cols = kManyCols - 1;
+  if (a.own == kFewRows && max_cols >= a.many_from) max_cols = a.many_from - 1;
   const int64_t all_pairs = (int64_t)a.b.num_seqs * a.b.h_kv;
   a.pair0 = 0;
   a.pairs = (int)all_pairs;
@@ -845,13 +845,22 @@ static void plan_one(KvAttnParams &a, bool f8) {
 
 int plan_kv_attention(const KvAttnParams &a, bool f8, KvAttnParams (&plan)[2]) {
   // The tcgen05 kernel multiplies 256 columns at a time (128 beyond 128 dimensions).
-  // It takes sequences of 64 columns or more, if the queries are bf16; its tensor
-  // map counts the cache's rows in 31 bits.
+  // It takes sequences of many_from columns or more, if the queries are bf16; its
+  // tensor map counts the cache's rows in 31 bits.
+  // It reads K and V once for all columns, the few-rows kernel once for every 8; but
+  // that one reads e4m3 as it is and divides short runs of keys further.  In us, few
+  // against many, 24 sequences of 4096 to 65536 tokens: bf16 16 columns 1256, 780;
+  // 32 columns 2178, 818; e4m3 32 columns 1479, 2070; 64 columns 2674, 2068.  64
+  // sequences with a window of 4096, bf16, 16 columns: 220, 272.  One of 4099 tokens:
+  // 25, 33.
+  const bool far = a.b.max_len >= 16384 && a.window >= a.b.max_len;
+  const int many_from = f8 ? 64 : far ? 16 : 24;
   const int64_t rows = (int64_t)a.b.num_pages * a.b.h_kv * a.b.page_tokens;
-  const bool many = a.q_bf16 && a.d >= 64 && (int64_t)a.b.max_rows * a.G >= kManyCols &&
+  const bool many = a.q_bf16 && a.d >= 64 && (int64_t)a.b.max_rows * a.G >= many_from &&
                     a.G <= 4096 && (f8 || rows < ((int64_t)1 << 31));
   plan[0] = a;
   plan[0].many_rows = many;
+  plan[0].many_from = many_from;
   plan[0].own = kEverySequence;
   plan[0].report = 1;
   // Sequences may have more rows or fewer (a prompt beside decoded tokens): those

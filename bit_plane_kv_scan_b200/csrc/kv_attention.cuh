@@ -13,9 +13,8 @@ namespace fathom {
 constexpr int prompt_cols(int d) { return d <= 128 ? 256 : 128; }
 constexpr int kPromptTile = 128;
 
-// From this many columns (rows times heads of a KV head) on a sequence goes to the
+// From many_from columns (rows times heads of a KV head) on a sequence goes to the
 // many-rows kernel.
-constexpr int kManyCols = 64;
 enum KvOwn { kEverySequence = 0, kFewRows = 1, kManyRows = 2 };
 
 struct KvAttnParams {
@@ -36,7 +35,8 @@ struct KvAttnParams {
   // tiles of `tile`, divided over `splits` thread blocks.
   int many_rows;  // the tcgen05 kernel
   int own;        // 0: every sequence; kFewRows, kManyRows: those with fewer than
-                  // kManyCols columns, the others
+                  // many_from columns, the others
+  int many_from;
   int report;     // this launch writes the status
   int cols, tile;
   // Units of one KV head: `dense`, col_tiles for each sequence; else sequence s
@@ -56,7 +56,7 @@ struct KvAttnParams {
 };
 
 __device__ __forceinline__ bool owns(const KvAttnParams &a, const KvSeq &q) {
-  return a.own == kEverySequence || (q.rows * a.G >= kManyCols) == (a.own == kManyRows);
+  return a.own == kEverySequence || (q.rows * a.G >= a.many_from) == (a.own == kManyRows);
 }
 
 // Unit y of a KV head: its sequence and which of the sequence's units it is.
