@@ -677,7 +677,11 @@ def _rows_of(x: torch.Tensor, name: str, rows: int, d: int) -> int:
     row, head, one = x.stride()
     if (one != 1 or (head != d and shape[1] > 1)) and x.numel():
         raise ValueError("%s: each row's heads must be contiguous" % name)
-    return row if rows > 1 else 0
+    if rows <= 1:
+        return 0
+    if row < shape[1] * d:  # (a broadcast row's stride is 0, which the library reads as contiguous)
+        raise ValueError("%s: rows overlap (row stride %d); copy a broadcast tensor first" % (name, row))
+    return row
 
 
 def _on(device: torch.device, *tensors: Optional[torch.Tensor]):
@@ -738,6 +742,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, 
     ks, vs = _rows_of(k, "k", rows, d), _rows_of(v, "v", rows, d)
     if k.shape[1] != cache.h_kv or v.shape[1] != cache.h_kv or v.dtype != k.dtype:
         raise ValueError("k and v must both be [num_rows, h_kv=%d, d] of one dtype" % cache.h_kv)
+    qs = 0 if q is None else _rows_of(q, "q", rows, d)
     pairs = 0
     if inv_freq is not None:
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -748,12 +753,12 @@ def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, 
         a.inv_freq, a.rotary_pairs, a.interleaved = inv_freq.data_ptr(), pairs, int(interleaved)
     with _Launch(device, stream) as at:
         if q is not None:
-            a.q_stride = _rows_of(q, "q", rows, d)
             if q_out is None:
                 q_out = at.new(q)
             elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and dtype")
             a.q, a.q_out, a.q_dtype, a.h_q = q.data_ptr(), q_out.data_ptr(), _dtype_code(q), q.shape[1]
+            a.q_stride = qs
         _check(lib().fathom_kv_append(ctypes.byref(a), at.raw))
     return q_out if q is not None else None
 
