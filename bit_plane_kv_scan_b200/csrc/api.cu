@@ -265,6 +265,12 @@ fathom_status check_rows(const char *name, int dtype, int heads, int d, int64_t 
   return FATHOM_OK;
 }
 
+// Whether bytes [a, a + na) and [b, b + nb) have one in common (NULL: nothing).
+bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && (x < y ? y - x < na : x - y < nb);
+}
+
 // Everything about an attention call but its pointers, and its plan.
 fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams (&plan)[2],
                                  int &plans) {
@@ -704,10 +710,9 @@ fathom_status fathom_kv_append(const fathom_kv_append_args *a, void *stream) {
     REQUIRE_ON_DEVICE(a->q_out, "q_out", el);
     const int64_t rows = a->batch.num_rows, row = (int64_t)a->h_q * d;
     const int64_t stride = a->q_stride ? a->q_stride : row;
-    const uintptr_t q0 = (uintptr_t)a->q, o0 = (uintptr_t)a->q_out;
-    const uintptr_t q1 = q0 + (uintptr_t)((rows - 1) * stride + row) * el;
-    const uintptr_t o1 = o0 + (uintptr_t)(rows * row) * el;
-    REQUIRE(q1 <= o0 || o1 <= q0 || (q0 == o0 && stride == row),
+    REQUIRE(!overlap(a->q, (uint64_t)((rows - 1) * stride + row) * el, a->q_out,
+                     (uint64_t)(rows * row) * el) ||
+                (a->q == a->q_out && stride == row),
             "q_out overlaps q without being q");
   }
   cudaError_t e = launch_kv_append(a, kv_batch_of(a->cache, a->batch), (cudaStream_t)stream);
@@ -730,10 +735,17 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   fathom_status st = check_kv_attention(a, plan, plans);
   if (st != FATHOM_OK) return st;
   if (plans == 0) return ok();  // no sequences or no rows
+  const size_t el = elt_size(a->q_dtype);
+  // a unit that is done again reads q after the first time has written out and lse
+  const uint64_t rows = a->batch.num_rows, row = (uint64_t)a->h_q * a->cache.d;
+  const uint64_t q_bytes = ((rows - 1) * (a->q_stride ? a->q_stride : row) + row) * el;
+  const uint64_t out_bytes = rows * row * el, lse_bytes = rows * a->h_q * 4;
+  REQUIRE(!overlap(a->q, q_bytes, a->out, out_bytes), "out overlaps q");
+  REQUIRE(!overlap(a->q, q_bytes, a->lse, lse_bytes), "lse overlaps q");
+  REQUIRE(!overlap(a->out, out_bytes, a->lse, lse_bytes), "lse overlaps out");
   const int dev = current_device();
   st = check_kv_pointers(a->cache, a->batch, dev);
   if (st != FATHOM_OK) return st;
-  const size_t el = elt_size(a->q_dtype);
   REQUIRE_ON_DEVICE(a->q, "q", el);
   REQUIRE_ON_DEVICE(a->out, "out", el);
   if (a->lse) REQUIRE_ON_DEVICE(a->lse, "lse", 4);

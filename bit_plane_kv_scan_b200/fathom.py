@@ -771,8 +771,8 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
     cache: every token up to the row's own, or with window > 0 the last `window` of
     them and the first `sinks`.
 
-    Returns (out [num_rows, h_q, d] of q's dtype, lse f32 [num_rows, h_q]); rows that
-    no sequence has are left as they were.  Without a workspace the call takes
+    Returns (out [num_rows, h_q, d] of q's dtype, lse f32 [num_rows, h_q]), neither of
+    which may overlap q; rows that no sequence has are left as they were.  Without a workspace the call takes
     one from torch's allocator, so that two captured graphs never share one."""
     device, rows, d = cache.device, batch.num_rows, cache.d
     _on(device, batch.page_table, q, out, lse)

@@ -535,7 +535,8 @@ FATHOM_API fathom_status fathom_kv_append(const fathom_kv_append_args *args, voi
  *   q    [num_rows][h_q][d] of q_dtype (FATHOM_BF16 or FATHOM_F32), rows
  *        q_stride elements apart (0: h_q * d).
  *   out  [num_rows][h_q][d] of q_dtype; lse float [num_rows][h_q] or NULL.
- *        Rows that no sequence has are left as they were.
+ *        Rows that no sequence has are left as they were.  q, out and lse must
+ *        not overlap.
  * Products run on the tensor cores with sums, maxima and softmax statistics in
  * fp32.  FATHOM_BF16 queries: softmax weights are rounded to 16 bits before they
  * meet V (bf16; fp16 where few rows read an FATHOM_E4M3 cache).  FATHOM_F32
