@@ -290,16 +290,17 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendParams 
   const int unit = blockIdx.x / p.parts, part0 = blockIdx.x % p.parts;
   int s = unit, u = 0;
   if (p.b.q_start) {
-    auto base = [&](int i) { return (int64_t)(p.b.q_start[i] >> 4) + 2 * (int64_t)i; };
-    s = find_seq(p.b.num_seqs, unit, base);
-    u = unit - (int)base(s);
+    auto base = [](int i, int row0) { return (int64_t)(row0 >> 4) + 2 * (int64_t)i; };
+    s = find_seq(p.b, unit, base);
+    u = (int)(unit - base(s, p.b.q_start[s]));
   }
   const KvSeq q = kv_seq(p.b, s);
+  if (u < 0 || u > q.rows / kKvBlock + 1) return;
   const int old = q.len - q.rows;  // tokens that the sequence had (< 0: more rows than tokens)
   // this unit's rows: those whose positions fall into one block of 16
   const int blk = (old >> 4) + u;  // floor: positions below 0 have blocks below 0
   const int p0 = max(blk * kKvBlock, old), p1 = min((blk + 1) * kKvBlock, q.len);
-  if (u < 0 || p1 <= p0) return;
+  if (p1 <= p0) return;
   const int row0 = q.row0 + (p0 - old), m = p1 - p0;
   const Turns lay(W, p.pairs, p.interleaved);
   bool have = false;

@@ -66,9 +66,9 @@ struct KvUnit {
 
 __device__ __forceinline__ KvUnit kv_unit(const KvAttnParams &a, int y) {
   if (a.dense) return {y / a.col_tiles, y % a.col_tiles};
-  auto base = [&](int i) { return (int64_t)a.b.q_start[i] * a.G / a.cols + i; };
-  const int s = find_seq(a.b.num_seqs, y, base);
-  const int64_t ct = y - base(s);
+  auto base = [&](int i, int row0) { return (int64_t)row0 * a.G / a.cols + i; };
+  const int s = find_seq(a.b, y, base);
+  const int64_t ct = y - base(s, a.b.q_start[s]);
   return {s, ct < 0 || ct >= a.col_tiles ? a.col_tiles : (int)ct};  // (col_tiles: none)
 }
 

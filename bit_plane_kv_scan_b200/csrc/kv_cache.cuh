@@ -25,6 +25,11 @@ struct KvSeq {
   bool valid;  // it kept every bound
 };
 
+// Rows r0 .. r1 - 1 keep the batch's bounds.
+__device__ __forceinline__ bool kv_rows_ok(const KvBatch &b, int r0, int r1) {
+  return r0 >= 0 && r1 >= r0 && r1 <= b.num_rows && r1 - r0 <= b.max_rows;
+}
+
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch &b, int s) {
   KvSeq q;
   const int n = b.seq_len[s];
@@ -35,7 +40,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch &b, int s) {
   bool r_ok = true;
   if (b.q_start) {
     const int r0 = b.q_start[s], r1 = b.q_start[s + 1];
-    r_ok = r0 >= 0 && r1 >= r0 && r1 <= b.num_rows && r1 - r0 <= b.max_rows;
+    r_ok = kv_rows_ok(b, r0, r1);
     q.row0 = r_ok ? r0 : 0;
     q.rows = r_ok ? r1 - r0 : 0;
   }
@@ -58,17 +63,37 @@ __device__ __forceinline__ int kv_scale_exp(uint32_t x) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// The sequence whose rows hold `row`: the last s with start(s) <= row, start
-// being non-decreasing.  The lanes of a warp look at 32 places at once.
+// The sequence that unit `x` belongs to, where sequence s starts at unit
+// start(s, q_start[s]): the last one that starts at x or before, of those whose rows
+// keep the bounds.  These start one behind the other as long as their rows do; what the
+// others' entries hold does not matter.  The lanes of a warp look at 32 places at once;
+// where a place on the way is one of the others, at every sequence in turn.
 template <typename Start>
-__device__ __forceinline__ int find_seq(int num_seqs, int64_t row, Start start) {
+__device__ __forceinline__ int find_seq(const KvBatch &b, int64_t x, Start start) {
+  constexpr uint32_t kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  int lo = 0, n = num_seqs;  // the answer is in [lo, lo + n)
+  bool ok;
+  auto starts_by = [&](int s) {  // (s past the last: no)
+    ok = true;
+    if (s >= b.num_seqs) return false;
+    const int r0 = b.q_start[s], r1 = b.q_start[s + 1];
+    ok = kv_rows_ok(b, r0, r1);
+    return ok && start(s, r0) <= x;
+  };
+  int lo = 0, n = b.num_seqs;  // the answer is in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
-    const int s = lo + lane * step;
-    const bool le = lane * step < n && start(s) <= row;
-    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    const bool inside = lane * step < n;
+    const bool le = starts_by(inside ? lo + lane * step : b.num_seqs);
+    if (step > 1 && !__all_sync(kAll, ok)) {
+      lo = 0;
+      for (int s = 0; s < b.num_seqs; s += 32) {
+        const uint32_t m = __ballot_sync(kAll, starts_by(s + lane));
+        if (m) lo = s + 31 - __clz((int)m);
+      }
+      return lo;
+    }
+    const uint32_t m = __ballot_sync(kAll, le);
     const int last = m ? 31 - __clz((int)m) : 0;
     n = min(step, n - last * step);
     lo += last * step;

@@ -469,7 +469,11 @@ typedef struct fathom_kv_cache {
  * or > max_len counts as empty, one whose rows are not within [0, num_rows) or
  * number more than max_rows as having no rows, and a page outside
  * [0, num_pages) or beyond table_width as holding nothing: its tokens are
- * neither written nor seen. */
+ * neither written nor seen.  The other sequences are served as ever, provided that
+ * their rows lie one behind the other; of sequences that claim the same rows, or
+ * rows before an earlier one's, any part may be left out.  fathom_kv_attention
+ * counts the sequences that break a bound as device faults; fathom_kv_append
+ * reports nothing. */
 typedef struct fathom_kv_batch {
   const int32_t *page_table;
   const int32_t *seq_len;
