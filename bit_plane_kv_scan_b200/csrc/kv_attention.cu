@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, TERMS > 1 || D > 128 ? 1 : F8 ? 4 : 
 }
 
 // After the many-rows kernel: the units that it marked, column tile by column
-// tile, each over all its keys.
+// tile, each over all its keys.  Its waits that ran out are added to the status here,
+// which is complete by now.
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
   grid_dependency_wait();
@@ -558,10 +559,14 @@ __global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
   b.tiles_per_split = 1 << 30;
   for (int x0 = blockIdx.x * kThreads; x0 < units; x0 += gridDim.x * kThreads) {
     // a thread looks at one unit's marks; marked ones are rare
-    int marked = 0;
+    int marked = 0, late = 0;
     if (x0 + (int)threadIdx.x < units)
-      for (int i = 0; i < a.splits; ++i)
-        marked |= a.taint[(int64_t)(x0 + threadIdx.x) * a.splits + i];
+      for (int i = 0; i < a.splits; ++i) {
+        const int mark = a.taint[(int64_t)(x0 + threadIdx.x) * a.splits + i];
+        marked |= mark;
+        late += (mark & kMarkLate) != 0;
+      }
+    if (late) atomicAdd(&a.status->device_faults, (uint32_t)late);
     if (!__syncthreads_or(marked)) continue;
     for (int k = 0; k < kThreads; ++k) {
       if (!__syncthreads_or(marked && (int)threadIdx.x == k)) continue;

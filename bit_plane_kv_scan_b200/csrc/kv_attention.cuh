@@ -17,6 +17,11 @@ constexpr int kPromptTile = 128;
 // many-rows kernel.
 enum KvOwn { kEverySequence = 0, kFewRows = 1, kManyRows = 2 };
 
+// What a block of the many-rows kernel leaves for the kernel that does units again:
+// do this one again, since a value of V that some row does not see is not finite; or
+// since a wait ran out, which is a device fault as well.
+constexpr int kMarkAgain = 1, kMarkLate = 2;
+
 struct KvAttnParams {
   KvBatch b;
   const void *ck, *cv;
@@ -50,7 +55,7 @@ struct KvAttnParams {
   int pair0, pairs, tail_from, box_rows, n_pad;
   const uint16_t *wide;  // [2][pairs][n_pad][d] bf16
   WsStatus *status;
-  int *taint;       // many_rows: [units * h_kv][splits], see kv_prompt.cu
+  int *taint;       // many_rows: [units * h_kv][splits] marks (kMarkAgain, kMarkLate)
   float2 *part_ml;  // [splits][num_rows * h_q]: maximum (log2 units), sum
   float *part_o;    // [splits][num_rows * h_q][d]
 };
@@ -115,7 +120,8 @@ __device__ __forceinline__ float lse_of(float m, float l, float shift) {
 }
 
 // The last block of a launch counts the sequences that break the batch's
-// bounds into the workspace's status.
+// bounds into the workspace's status.  (Nothing else of that launch may write there:
+// its other blocks come before or after this one in no particular order.)
 __device__ __forceinline__ void write_status(const KvAttnParams &a) {
   __shared__ int bad;
   if (threadIdx.x == 0) bad = 0;

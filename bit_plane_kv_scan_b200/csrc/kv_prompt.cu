@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (bad) *taint = 1;
+          if (bad) *taint = kMarkAgain;
           proxy_fence();
         }
         mbar_arrive(v_ready(st));
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (tid == 0 && s_fault) atomicAdd(&a.status->device_faults, 1u);
+  if (tid == 0 && s_fault) *taint |= kMarkLate;
   tc_fence_after();
   if (warp == kMmaWarp && s_fault) {  // given up halfway: what was issued ends first
     const long long t0 = clock64();

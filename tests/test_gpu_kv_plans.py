@@ -1,0 +1,101 @@
+"""fathom_kv_attention on the GPU over calls whose launches are divided, grouped or
+bounded in less usual ways, against fp64."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_kv as T
+from test_gpu_kv import BF16, F32, F8, WEIGHT, _lib, make_batch, make_cache, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attention64(cache, table, seqs, q, scale, window=0, sinks=0, weight_step=2.0 ** -8, out_step=2.0 ** -8):
+    """The formula in fp64 on the GPU, with kv_reference.py's tolerances: (out, lse, tolerance of
+    out, tolerance of lse).  weight_step 2^-11 stands for fp16 weights, which have 11 bits down to
+    2^-29 of the largest and are off by 2^-40 of it below: 2^-40 sum |v| more."""
+    rows, h_q, d = q.shape
+    h_kv, page = cache.k.shape[1], cache.page_tokens
+    G = h_q // h_kv
+    dev = q.device
+    out, tol = (torch.zeros((rows, h_q, d), dtype=torch.float64, device=dev) for _ in range(2))
+    lse, ltol = (torch.zeros((rows, h_q), dtype=torch.float64, device=dev) for _ in range(2))
+    held = torch.zeros(rows, dtype=torch.bool, device=dev)
+    q = q.double()
+    for s, (row0, m, n) in enumerate(seqs):
+        if m == 0:
+            continue
+        held[row0:row0 + m] = True
+        j = torch.arange(n, device=dev)
+        pg = torch.as_tensor(np.asarray(table[s]), device=dev).long()[j // page]
+        sl = j % page
+        for g in range(h_kv):
+            kv = []
+            for name in ("k", "v"):
+                x = getattr(cache, name)
+                if x.dtype == F8:
+                    x = x.view(torch.uint8)[pg, g, sl].view(F8).double()
+                    e = getattr(cache, name + "_scale")[pg, g, sl // 16].double().clamp(8, 246)
+                    x = x * torch.exp2(e - 127)[:, None]
+                else:
+                    x = x[pg, g, sl].double()
+                kv.append(x)
+            k, v = kv
+            heads = slice(g * G, (g + 1) * G)
+            for r in range(0, m, 256):
+                e = min(m, r + 256)
+                at = slice(row0 + r, row0 + e)
+                p = torch.arange(n - m + r, n - m + e, device=dev)[:, None]
+                see = j <= p
+                if window:
+                    see &= (j > p - window) | (j < sinks)
+                see = see[:, None, :]
+                qq = q[at, heads]
+                sc = (qq @ k.T * scale).masked_fill(~see, -math.inf)
+                lse[at, heads] = torch.logsumexp(sc, -1)
+                w = torch.softmax(sc, -1)
+                out[at, heads] = w @ v
+                a = w @ v.abs()
+                b = (abs(scale) * (qq.abs() @ k.abs().T)).masked_fill(~see, 0.0).amax(-1)
+                count = see.sum(-1)
+                delta = (d / 16 + 4) * 2.0 ** -22 * b
+                adds = count / 16 + 16
+                tol[at, heads] = (2 * (delta[..., None] + 2.0 ** -20) + weight_step + adds[..., None] * 2.0 ** -22) * a \
+                    + out_step * out[at, heads].abs() + 1e-30
+                if weight_step == 2.0 ** -11:
+                    tol[at, heads] += 2.0 ** -40 * (see.double() @ v.abs())
+                ltol[at, heads] = delta + 2.0 ** -20 + adds * 2.0 ** -23 + 2.0 ** -22 * lse[at, heads].abs().clamp(min=1)
+    return out, lse, tol, ltol, held
+
+
+def check(got, want, what=""):
+    out, lse, tol, ltol, held = want
+    e = ((got[0].double() - out).abs() / tol.clamp(min=1e-30))[held].max().item()
+    assert e <= 1, "%s: out off by %g tolerances" % (what, e)
+    e = ((got[1].double() - lse).abs() / ltol.clamp(min=1e-30))[held].max().item()
+    assert e <= 1, "%s: lse off by %g tolerances" % (what, e)
+
+
+def test_status_of_a_call_with_more_units_than_processors():
+    """A prompt of several hundred units beside sequences that break their bounds: all of these
+    are counted, and a good call clears them."""
+    rng = np.random.default_rng(50)
+    cache = make_cache(rng, 120, 64, 8, 64, BF16)
+    table = torch.from_numpy(rng.permutation(120).astype(np.int32)[None].repeat(4, 0)).cuda()
+    start = torch.tensor([0, 3000, 3001, 3001, 3002], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([7000, -1, 9000, 3], dtype=torch.int32, device="cuda")
+    batch = T.F.KVBatch(table, lens, start, num_rows=3002, max_rows=3000)
+    q = randn(rng, 3002, 32, 64)
+    ws = T.F.Workspace()
+    got = T.F.kv_attention(cache, batch, q, workspace=ws)
+    with pytest.raises(T.F.FathomError, match="2 faults"):
+        T.F.check_device_status(ws)
+    want = attention64(cache, table.cpu().numpy(), [(0, 3000, 7000), (0, 0, 0), (0, 0, 0), (3001, 1, 3)], q, 1 / 8)
+    check(got, want)
+    assert (got[0][3000] == 0).all() and torch.isneginf(got[1][3000]).all()
+    lens.copy_(torch.tensor([7000, 1, 0, 3], dtype=torch.int32))
+    T.F.kv_attention(cache, batch, q, workspace=ws)
+    T.F.check_device_status(ws)
