@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (page * a.b.h_kv + head) * a.b.page_tokens + key % a.b.page_tokens;
   };
   int next_box = warp == kTmaWarp && nt > 0 ? place(0) : -1;
+  int issued = 2 * nt;  // of K's and V's tiles, in turn: those that TMA begins to fetch
   auto load = [&](int j) {
     const int at = next_box;
     if (j + 1 < nt) next_box = place(j + 1);
@@ -372,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const int x = 2 * j + side, st = x % kStages;
-      if (x >= kStages && !warp_wait(kv_empty(st), (x / kStages - 1) & 1)) return false;
+      if (x >= kStages && !warp_wait(kv_empty(st), (x / kStages - 1) & 1)) {
+        issued = x;
+        return false;
+      }
       if (lane == 0) mbar_expect(kv_full(st), n * a.box_rows * 128);
       __syncwarp();
       if (at >= 0)
@@ -623,10 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool live = true;
       for (int j = kStages / 2; j < nt && live; ++j) live = load(j);
       if (!live) s_fault = 1;
-      // no copy may be on its way when the block ends: the last ones are waited for
-      // by their readers, or here when those have given up
-      if (!live)
-        for (int i = 0; i < kStages; ++i) mbar_wait(kv_full(i), 0);
+      // No copy may be on its way when the block ends, whoever has given up by then:
+      // each place's last one is waited for here too.
+      for (int i = 0; i < kStages && i < issued; ++i)
+        mbar_wait(kv_full(i), ((issued - 1 - i) / kStages) & 1);
     } else if (warp >= kEdgeWarp0 && nt > 0) {
       // ------------------------------------------------------- V's edges --
       const int t = tid - 32 * kEdgeWarp0;
