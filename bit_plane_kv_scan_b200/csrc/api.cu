@@ -310,15 +310,16 @@ fathom_status check_kv_attention(const fathom_kv_attention_args *a, KvAttnParams
   return FATHOM_OK;
 }
 
-// The workspace: status, then for each launch the units' marks, the splits' maxima
-// and sums and their outputs, and the widened keys and values.  Returns its size; with
+// The workspace: status, then for each launch the units' marks, the divided units'
+// maxima, sums and outputs, and the widened keys and values.  Returns its size; with
 // a base address, the launches learn where their parts are.
 size_t kv_workspace(KvAttnParams (&plan)[2], int plans, unsigned char *base) {
   size_t at = sizeof(WsStatus);
   for (int i = 0; i < plans; ++i) {
     KvAttnParams &p = plan[i];
-    const size_t parts =
-        p.splits > 1 && !p.cluster ? (size_t)p.splits * p.b.num_rows * p.h_q : 0;
+    const size_t parts = p.splits > 1 && !p.cluster
+                             ? (size_t)((int64_t)p.units * p.b.h_kv - p.tail_from) * p.splits * p.part_cols
+                             : 0;
     const size_t marks = p.many_rows ? (size_t)p.units * p.b.h_kv * p.splits : 0;
     if (base) {
       p.status = reinterpret_cast<WsStatus *>(base);

@@ -205,10 +205,11 @@ __device__ __forceinline__ void add_pv(float (&o)[D / 16][4], const uint32_t (&v
   }
 }
 
-// One thread block's share: column tile ct of sequence s and KV head `head`, the
-// split-th run of its keys.
+// One thread block's share: column tile ct of sequence s and KV head `head`, which is
+// unit `unit`, the split-th run of its keys.
 template <int D, bool F8, int TERMS>
-__device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, int ct, int split) {
+__device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, int ct, int unit,
+                                       int split) {
   using S = Shape<D, F8>;
   constexpr int kSteps = D / 16;
   constexpr float kShift = F8 ? 15.0f : 0.0f;
@@ -501,7 +502,7 @@ __device__ __forceinline__ void attend(const KvAttnParams &a, int s, int head, i
       store_out(a, rh * D + dim, L > 0.0f ? O / L : (L == 0.0f ? 0.0f : L));
       if (dim == 0 && a.lse) a.lse[rh] = lse_of(M, L, kShift);
     } else {
-      const int64_t part = (int64_t)split * a.b.num_rows * a.h_q + rh;
+      const int64_t part = part_at(a, unit, split) + c;
       a.part_o[part * D + dim] = O;
       if (dim == 0) a.part_ml[part] = make_float2(M, L);
     }
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, TERMS > 1 || D > 128 ? 1 : F8 ? 4 : 
   const int split = x % a.splits;
   x /= a.splits;
   const KvUnit u = kv_unit(a, x / a.b.h_kv);
-  attend<D, F8, TERMS>(a, u.s, x % a.b.h_kv, u.ct, split);
+  attend<D, F8, TERMS>(a, u.s, x % a.b.h_kv, u.ct, x, split);
 }
 
 // After the many-rows kernel: the units that it marked, column tile by column
@@ -574,23 +575,22 @@ __global__ void __launch_bounds__(kThreads) kv_redo_kernel(KvAttnParams a) {
       const KvSeq q = kv_seq(a.b, u.s);
       const int rb = (q.rows * a.G + a.cols - 1) / a.cols - 1 - u.ct;  // (units come last first)
       for (int ct = 0; ct < per; ++ct) {
-        attend<D, F8, 1>(b, u.s, (x0 + k) % a.b.h_kv, rb * per + ct, 0);
+        attend<D, F8, 1>(b, u.s, (x0 + k) % a.b.h_kv, rb * per + ct, x0 + k, 0);
         __syncthreads();
       }
     }
   }
 }
 
-// One warp's part in joining the splits of one (row, head): of n splits those from
-// `from` on, every `step`-th; lane l has dimensions l, l + 32, ...  The splits' maxima
+// One warp's part in joining the splits of one column of a unit, the first split's
+// result being number `at`: of n splits those from `from` on, every `step`-th; lane l has dimensions l, l + 32, ...  The splits' maxima
 // and sums are read 32 at a time, their outputs 8 at a time, so that their latency
 // is not paid split by split.
 template <int D>
-__device__ __forceinline__ void join_splits(const KvAttnParams &a, int64_t rh, int n, int from,
+__device__ __forceinline__ void join_splits(const KvAttnParams &a, int64_t at, int n, int from,
                                             int step, float &m, float &l, float (&o)[D / 32]) {
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.b.num_rows * a.h_q;
   const int mine = n > from ? (n - from + step - 1) / step : 0;
   m = -INFINITY;
   l = 0.0f;
@@ -598,7 +598,7 @@ __device__ __forceinline__ void join_splits(const KvAttnParams &a, int64_t rh, i
   for (int j = 0; j < kPer; ++j) o[j] = 0.0f;
   for (int i0 = 0; i0 < mine; i0 += 32) {
     const int split = from + step * (i0 + lane);
-    const float2 ml = split < n ? a.part_ml[split * rows + rh] : make_float2(-INFINITY, 0.0f);
+    const float2 ml = split < n ? a.part_ml[at + (int64_t)split * a.part_cols] : make_float2(-INFINITY, 0.0f);
     float big = ml.x;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
@@ -618,7 +618,8 @@ __device__ __forceinline__ void join_splits(const KvAttnParams &a, int64_t rh, i
       float v[8][kPer];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float *po = a.part_o + ((from + step * (int64_t)(i0 + k0 + k)) * rows + rh) * D + lane;
+        const float *po =
+            a.part_o + (at + (from + step * (int64_t)(i0 + k0 + k)) * a.part_cols) * D + lane;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[k][j] = k0 + k < here ? po[32 * j] : 0.0f;
       }
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(KvAttnParams a, float
   const KvTiles tiles = visible_tiles(a, first + c0 / a.G, first + (c1 - 1) / a.G, a.tile);
   const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
   float m, l, o[D / 32];
-  join_splits<D>(a, rh, n, warp, kWarps, m, l, o);
+  join_splits<D>(a, part_at(a, x, 0) + (col - c0), n, warp, kWarps, m, l, o);
   if (lane == 0) {
     s_m[warp] = m;
     s_l[warp] = l;
@@ -693,7 +694,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_units_kernel(KvAttnParams a)
   const int n = max(1, (tiles.count + a.tiles_per_split - 1) / a.tiles_per_split);
   const int64_t rh = (int64_t)(q.row0 + col / a.G) * a.h_q + head * a.G + col % a.G;
   float m, l, o[D / 32];
-  join_splits<D>(a, rh, n, 0, 1, m, l, o);
+  join_splits<D>(a, part_at(a, x, 0) + (col - c0), n, 0, 1, m, l, o);
 #pragma unroll
   for (int j = 0; j < D / 32; ++j)
     store_out(a, rh * D + 32 * j + lane, l > 0.0f ? o[j] / l : (l == 0.0f ? 0.0f : l));
@@ -795,6 +796,7 @@ static void plan_one(KvAttnParams &a, bool f8) {
   }
   a.cols = a.many_rows ? prompt_cols(d) : kCols;
   a.tile = a.many_rows ? kPromptTile : kKvBlock;
+  a.part_cols = (int)(max_cols < a.cols ? max_cols : a.cols);
   a.col_tiles = (int)((max_cols + a.cols - 1) / a.cols);
   const int64_t dense = (int64_t)a.b.num_seqs * a.col_tiles;
   const int64_t packed = (int64_t)a.b.num_rows * a.G / a.cols + a.b.num_seqs;

@@ -56,8 +56,11 @@ struct KvAttnParams {
   const uint16_t *wide;  // [2][pairs][n_pad][d] bf16
   WsStatus *status;
   int *taint;       // many_rows: [units * h_kv][splits] marks (kMarkAgain, kMarkLate)
-  float2 *part_ml;  // [splits][num_rows * h_q]: maximum (log2 units), sum
-  float *part_o;    // [splits][num_rows * h_q][d]
+  // of the units from tail_from on, if they are divided and no cluster: [unit]
+  // [split][part_cols], part_cols the most columns that a unit has
+  int part_cols;
+  float2 *part_ml;  // maximum (log2 units), sum
+  float *part_o;    // [d] each
 };
 
 __device__ __forceinline__ bool owns(const KvAttnParams &a, const KvSeq &q) {
@@ -75,6 +78,11 @@ __device__ __forceinline__ KvUnit kv_unit(const KvAttnParams &a, int y) {
   const int s = find_seq(a.b, y, base);
   const int64_t ct = y - base(s, a.b.q_start[s]);
   return {s, ct < 0 || ct >= a.col_tiles ? a.col_tiles : (int)ct};  // (col_tiles: none)
+}
+
+// Where split `split` of unit `unit` (of all KV heads') leaves its result for column 0.
+__device__ __forceinline__ int64_t part_at(const KvAttnParams &a, int unit, int split) {
+  return ((int64_t)(unit - a.tail_from) * a.splits + split) * a.part_cols;
 }
 
 // Whether a row at position p sees token j.

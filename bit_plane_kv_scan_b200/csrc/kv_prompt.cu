@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t rh = (int64_t)row * a.h_q + h;
       const bool mine = c < c1;
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-      const int64_t part = (int64_t)split * a.b.num_rows * a.h_q + rh;
+      const int64_t part = part_at(a, u.unit, split) + (c - c0);
 #pragma unroll
       for (int i = 0; i < DP / 32; ++i) {
         if (32 * i >= d) break;

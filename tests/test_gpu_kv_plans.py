@@ -99,3 +99,46 @@ def test_status_of_a_call_with_more_units_than_processors():
     lens.copy_(torch.tensor([7000, 1, 0, 3], dtype=torch.int32))
     T.F.kv_attention(cache, batch, q, workspace=ws)
     T.F.check_device_status(ws)
+
+
+def _size(cache, batch, q, **kw):
+    """Bytes of the workspace that the call asks for."""
+    ws = T.F.Workspace()
+    got = T.F.kv_attention(cache, batch, q, workspace=ws, **kw)
+    return got, ws.buf.numel()
+
+
+DIVIDED = [
+    # d, h_kv, G, lens, rows, window, sinks
+    (128, 1, 4, [9000], [100], 0, 0),           # fewer units than processors: each is divided
+    (64, 2, 4, [7000, 3000], [130, 64], 0, 0),
+    (96, 1, 8, [6000], [40], 2500, 300),
+    (256, 1, 4, [5000], [70], 0, 0),
+    (128, 8, 4, [5200], [1270], 0, 0),          # 160 units on 148 processors: the last 12 are
+    (64, 8, 4, [4500], [1265], 3000, 5),
+    (256, 8, 4, [2500], [600], 0, 0),           # 152 units
+    (160, 8, 2, [4000], [1200], 0, 0),          # 152 units of unequal work: not divided
+    (160, 8, 2, [5000], [1200], 0, 0),          # of about equal work (a context of 4 times the rows)
+    (128, 1, 4, [60000], None, 0, 0),           # a decoded token: more splits than a cluster has
+    (64, 1, 2, [40000, 33, 9000], [1, 2, 3], 0, 0),
+    (128, 2, 4, [3000, 40000, 20000], [800, 1, 3], 0, 0),   # both kernels
+    (128, 2, 4, [3000, 40000, 20000], [800, 1, 3], 15000, 4),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("d,h_kv,G,lens,rows,window,sinks", DIVIDED)
+def test_divided_units(d, h_kv, G, lens, rows, window, sinks, qt, dtype):
+    rng = np.random.default_rng(51)
+    ct, qt = BF16 if dtype == "bf16" else F8, BF16 if qt == "bf16" else F32
+    pages = sum(-(-n // 128) for n in lens)
+    cache = make_cache(rng, pages, 128, h_kv, d, ct)
+    batch, table, seqs = make_batch(rng, pages, 128, lens, rows)
+    q = randn(rng, batch.num_rows, h_kv * G, d, dtype=qt, scale=1.5)
+    got, size = _size(cache, batch, q, window=window, sinks=sinks)
+    if (ct, qt) == (BF16, BF16) and not window and (lens, d) != ([4000], 160):
+        assert size > 2 * 8 * (d + 2) * 4 * G  # divided: there are results to join
+    want = attention64(cache, table, seqs, q, 1 / math.sqrt(d), window, sinks, WEIGHT[ct, qt],
+                       2.0 ** -8 if qt == BF16 else 2.0 ** -24)
+    check(got, want)
