@@ -365,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (page * a.b.h_kv + head) * a.b.page_tokens + key % a.b.page_tokens;
   };
   int next_box = warp == kTmaWarp && nt > 0 ? place(0) : -1;
-  int issued = 2 * nt;  // of K's and V's tiles, in turn: those that TMA begins to fetch
   auto load = [&](int j) {
     const int at = next_box;
     if (j + 1 < nt) next_box = place(j + 1);
@@ -373,10 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const int x = 2 * j + side, st = x % kStages;
-      if (x >= kStages && !warp_wait(kv_empty(st), (x / kStages - 1) & 1)) {
-        issued = x;
-        return false;
-      }
+      if (x >= kStages && !warp_wait(kv_empty(st), (x / kStages - 1) & 1)) return false;
       if (lane == 0) mbar_expect(kv_full(st), n * a.box_rows * 128);
       __syncwarp();
       if (at >= 0)
@@ -627,10 +623,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool live = true;
       for (int j = kStages / 2; j < nt && live; ++j) live = load(j);
       if (!live) s_fault = 1;
-      // No copy may be on its way when the block ends, whoever has given up by then:
-      // each place's last one is waited for here too.
-      for (int i = 0; i < kStages && i < issued; ++i)
-        mbar_wait(kv_full(i), ((issued - 1 - i) / kStages) & 1);
     } else if (warp >= kEdgeWarp0 && nt > 0) {
       // ------------------------------------------------------- V's edges --
       const int t = tid - 32 * kEdgeWarp0;
@@ -765,7 +757,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (tid == 0 && s_fault) *taint |= kMarkLate;
   tc_fence_after();
-  if (warp == kMmaWarp && s_fault) {  // given up halfway: what was issued ends first
+  // Given up halfway: what was issued, products and copies, ends first.  A wait gives up
+  // after 2^31 clocks, in which whoever feeds it has stopped too, so the last copy is a
+  // second old by now; 2^24 clocks more are a hundred times what one takes.  (Waits on
+  // the copies' own barriers here make the compiler spill: 0.8% on every call.)
+  if (warp == kMmaWarp && s_fault) {
     const long long t0 = clock64();
     while (clock64() - t0 < (1ll << 24)) {
     }
