@@ -775,6 +775,17 @@ static int kv_resident_blocks(int d, bool f8) {
   return 148 * (per > 4 ? 4 : per);
 }
 
+// The most tiles of `tile` keys that `rows` tokens in a row can see, at least 1.
+static int64_t most_tiles(const KvAttnParams &a, int64_t rows, int tile) {
+  int64_t most = ((int64_t)a.b.max_len + tile - 1) / tile;
+  if (a.window < a.b.max_len) {
+    const int64_t w = ((int64_t)a.window + rows - 1 + tile - 2) / tile + 1 +
+                      ((int64_t)a.sinks + tile - 1) / tile;
+    if (w < most) most = w;
+  }
+  return most < 1 ? 1 : most;
+}
+
 // One launch's plan: of the few-rows or the many-rows kernel, for a.own's sequences.
 static void plan_one(KvAttnParams &a, bool f8) {
   const int d = a.d;
@@ -786,9 +797,9 @@ static void plan_one(KvAttnParams &a, bool f8) {
   a.n_pad = 0;
   a.box_rows = kPromptTile;
   if (a.many_rows && f8) {
-    // The widened copy holds as many pairs at a time as fit in 4 GiB.
-    a.n_pad = (int)(((int64_t)a.b.max_len + kPromptTile - 1) / kPromptTile * kPromptTile);
-    if (a.n_pad == 0) a.n_pad = kPromptTile;
+    // The widened copy holds as many pairs at a time as fit in 4 GiB, of each the tiles
+    // that some row may see.
+    a.n_pad = (int)(most_tiles(a, a.b.max_rows, kPromptTile) * kPromptTile);
     const int64_t fit = ((int64_t)4 << 30) / ((int64_t)a.n_pad * d * 4);
     a.pairs = (int)(fit < 1 ? 1 : fit < all_pairs ? fit : all_pairs);
   } else if (a.many_rows) {
@@ -805,15 +816,8 @@ static void plan_one(KvAttnParams &a, bool f8) {
   a.units = (int)(units < INT32_MAX ? units : INT32_MAX);  // (the caller checks the launch's size)
   // the most tiles that one unit's columns can see
   const int64_t tokens = (a.cols + a.G - 2) / a.G + 1;  // tokens that `cols` columns can span
-  int64_t most = ((int64_t)a.b.max_len + a.tile - 1) / a.tile;
-  bool windowed = false;
-  if (a.window < a.b.max_len) {
-    const int64_t w = ((int64_t)a.window + tokens - 1 + a.tile - 2) / a.tile + 1 +
-                      ((int64_t)a.sinks + a.tile - 1) / a.tile;
-    windowed = w < most;
-    if (windowed) most = w;
-  }
-  if (most < 1) most = 1;
+  const int64_t most = most_tiles(a, tokens, a.tile);
+  const bool windowed = most < ((int64_t)a.b.max_len + a.tile - 1) / a.tile;
   const int64_t base = units * a.b.h_kv;
   int64_t splits;
   a.tail_from = 0;

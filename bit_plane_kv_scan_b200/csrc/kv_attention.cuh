@@ -51,7 +51,8 @@ struct KvAttnParams {
   int cluster;  // few rows: a unit's splits are a cluster
   // many_rows: the (sequence, KV head) pairs of one launch; the units in order of
   // work from which on they are divided (the others are not); the rows of a K or V
-  // box; e4m3: tokens of a pair in the widened copy (0: there is none)
+  // box; e4m3: keys of a pair in the widened copy, the tiles that its rows see (KvTiles'
+  // order) one behind the other (0: there is none)
   int pair0, pairs, tail_from, box_rows, n_pad;
   const uint16_t *wide;  // [2][pairs][n_pad][d] bf16
   WsStatus *status;
@@ -95,6 +96,8 @@ __device__ __forceinline__ bool sees(const KvAttnParams &a, int p, int j) {
 struct KvTiles {
   int count, sink_tiles, skip;
   __device__ __forceinline__ int at(int i) const { return i < sink_tiles ? i : i + skip; }
+  // which one tile t is, of these rows' or of some of them alone
+  __device__ __forceinline__ int index(int t) const { return t < sink_tiles ? t : t - skip; }
 };
 
 __device__ __forceinline__ KvTiles visible_tiles(const KvAttnParams &a, int p_lo, int p_hi,

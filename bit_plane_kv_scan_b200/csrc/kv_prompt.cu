@@ -354,12 +354,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // one page, 64 dimensions).  False if the ring's places did not become free.
   const int panels = (d + 63) / 64;
   const int box_row = lane / panels * a.box_rows, box_panel = lane % panels;
+  // where the widened copy has the sequence's tiles
+  const KvTiles wide = visible_tiles(a, first, q.len - 1, kN);
   auto place = [&](int j) {  // the box's row in the tensor map; -1: nothing to fetch
-    const int key = kN * tiles.at(i0 + j) + box_row, last = key + a.box_rows - 1;
+    const int tile = tiles.at(i0 + j), key = kN * tile + box_row, last = key + a.box_rows - 1;
     if (lane >= kN / a.box_rows * panels || key > p_hi ||
         (last <= p_lo - a.window && key >= a.sinks))
       return -1;
-    if (a.n_pad > 0) return (pair - a.pair0) * a.n_pad + key;
+    if (a.n_pad > 0) return (pair - a.pair0) * a.n_pad + kN * wide.index(tile) + box_row;
     const int page = page_of(key);
     if (page < 0) return -1;
     return (page * a.b.h_kv + head) * a.b.page_tokens + key % a.b.page_tokens;
@@ -783,12 +785,13 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
   allow_dependent_launch();
   const int d = a.d, pieces = d / 16;
   const int per = a.n_pad / kN;
-  const int pair = blockIdx.x / per, key0 = blockIdx.x % per * kN;
+  const int pair = blockIdx.x / per, tile = blockIdx.x % per;
   const int head = (a.pair0 + pair) % a.b.h_kv, s = (a.pair0 + pair) / a.b.h_kv;
   const KvSeq q = kv_seq(a.b, s);
-  if (q.rows == 0 || key0 >= q.len || !owns(a, q)) return;
-  const int from = q.len - q.rows - a.window;  // the last key before every row's window
-  if (key0 + kN - 1 <= from && key0 >= a.sinks) return;
+  if (q.rows == 0 || !owns(a, q)) return;
+  const KvTiles tiles = visible_tiles(a, q.len - q.rows, q.len - 1, kN);
+  if (tile >= tiles.count) return;
+  const int key0 = tiles.at(tile) * kN;
   for (int i = threadIdx.x; i < kN * pieces; i += kWidenThreads) {
     const int r = (int)((unsigned)i / (unsigned)pieces), piece = i - r * pieces, key = key0 + r;
     if (key >= q.len) return;
@@ -799,7 +802,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
     const int64_t h = (int64_t)page * a.b.h_kv + head;
     const int64_t src = (h * a.b.page_tokens + slot) * d + piece * 16;
     const int64_t sc = h * (a.b.page_tokens / kKvBlock) + slot / kKvBlock;
-    const int64_t dst = ((int64_t)pair * a.n_pad + key) * d + piece * 16;
+    const int64_t dst = ((int64_t)pair * a.n_pad + tile * kN + r) * d + piece * 16;
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const uint4 v = __ldg(reinterpret_cast<const uint4 *>(

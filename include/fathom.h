@@ -549,8 +549,8 @@ FATHOM_API fathom_status fathom_kv_append(const fathom_kv_append_args *args, voi
  * sinks >= 0.  The workspace (fathom_kv_attention_workspace_size bytes, 0 on
  * bad arguments) is 256-byte aligned device memory, which the call need not
  * find cleared; calls sharing one must not overlap.  (Many rows over an
- * FATHOM_E4M3 cache need up to 4 GiB of it, for the keys and values widened to
- * bf16, or one KV head of one sequence where that is more.)  It starts with the status
+ * FATHOM_E4M3 cache need up to 4 GiB of it, for the keys and values that a sequence's
+ * rows may see widened to bf16, or one KV head of one sequence where that is more.)  It starts with the status
  * that fathom_check_device_status reads: a sequence that the batch's bounds
  * reject is a device fault, and so is a wait inside a kernel that ran out.
  */

@@ -142,3 +142,35 @@ def test_divided_units(d, h_kv, G, lens, rows, window, sinks, qt, dtype):
     want = attention64(cache, table, seqs, q, 1 / math.sqrt(d), window, sinks, WEIGHT[ct, qt],
                        2.0 ** -8 if qt == BF16 else 2.0 ** -24)
     check(got, want)
+
+
+WIDENED = [
+    # d, h_kv, G, page, lens, rows, window, sinks, max_len
+    (128, 2, 4, 64, [9000, 700, 5000], [300, 200, 64], 1000, 0, 1 << 20),
+    (64, 1, 8, 48, [4000, 300, 131], [150, 299, 131], 513, 700, 1 << 20),  # more first tokens than a window
+    (96, 2, 2, 16, [2500], [1500], 100, 130, 1 << 18),
+    (256, 1, 4, 128, [3000, 2000], [400, 300], 640, 5, 1 << 20),
+    (128, 1, 4, 32, [6000], [5000], 128, 1, 1 << 16),
+    (128, 2, 4, 64, [900, 300, 17, 1500, 64, 2000], [300, 200, 17, 100, 64, 40], 0, 0, 1 << 20),  # two groups of pairs
+    (256, 2, 8, 128, [600, 1000, 70], [100, 8, 70], 0, 0, 1 << 20),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,h_kv,G,page,lens,rows,window,sinks,max_len", WIDENED)
+def test_bounds_far_above_the_lengths(d, h_kv, G, page, lens, rows, window, sinks, max_len, dtype):
+    """What the host sizes by max_len holds whatever the lengths are: over e4m3 the tiles that
+    a window sees lie one behind the other in the widened copy, and pairs that do not fit into
+    4 GiB come in groups."""
+    rng = np.random.default_rng(52)
+    ct = BF16 if dtype == "bf16" else F8
+    pages = sum(-(-n // page) for n in lens) + 1
+    cache = make_cache(rng, pages, page, h_kv, d, ct)
+    batch, table, seqs = make_batch(rng, pages, page, lens, rows, max_len=max_len)
+    q = randn(rng, batch.num_rows, h_kv * G, d, scale=1.5)
+    got = T.F.kv_attention(cache, batch, q, window=window, sinks=sinks)
+    want = attention64(cache, table, seqs, q, 1 / math.sqrt(d), window, sinks, WEIGHT[ct, BF16])
+    check(got, want)
+    exact = T.F.KVBatch(batch.page_table, batch.seq_len, batch.q_start, num_rows=batch.num_rows,
+                        max_rows=batch.max_rows, max_len=max(lens))
+    check(T.F.kv_attention(cache, exact, q, window=window, sinks=sinks), want)

@@ -41,3 +41,13 @@ def test_decoded_tokens_beside_a_long_prompt(L):
     # the few-rows launch leaves results for the columns that it may have, not for the prompt's
     assert size(L, 8193, 8192, 1 << 20, seqs=2) <= 64 * MB
     assert size(L, 64 * 1000 + 63, 64000, 1 << 20, seqs=64) <= 64 * MB
+
+
+def test_widened_keys_are_those_that_a_window_sees(L):
+    # 49 tiles of 128 keys for the window and the rows, 8 KV heads, K and V in bf16: 26 MB
+    loose = size(L, 2048, 2048, 1 << 20, dtype=F.E4M3, window=4096)
+    assert loose <= 64 * MB
+    assert size(L, 2048, 2048, 1 << 20, dtype=F.E4M3, window=4096, sinks=300) > loose
+    # where everything is seen: at most 4 GiB, or one pair
+    assert size(L, 2048, 2048, 1 << 20, dtype=F.E4M3) <= (4 << 30) + 64 * MB
+    assert size(L, 2048, 2048, 1 << 20, dtype=F.E4M3) >= 4 << 30
