@@ -340,15 +340,27 @@ def sparse_attention(q: torch.Tensor, k_rows: Optional[torch.Tensor], v_rows: to
 
 
 class Workspace:
-    """A reusable device workspace that grows to the largest request."""
+    """A reusable device workspace that grows to the largest request.
+
+    A buffer that grows is dropped for a new one.  The allocator is told of every stream
+    that a buffer was used on beside the one that it was allocated for, so that it does
+    not hand a dropped one out before these have passed."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = torch.empty(0, dtype=torch.uint8, device=self.device)
+        self._home = None  # the handle of the stream that buf was allocated for
 
-    def get(self, nbytes: int) -> torch.Tensor:
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        """nbytes for a call on `stream` (None: torch's current stream)."""
+        device = self.buf.device
+        raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
         if self.buf.numel() < nbytes:
-            self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(stream):
+                self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+            self._home = raw
+        elif raw != self._home:
+            self.buf.record_stream(torch.cuda.current_stream(device) if stream is None else stream)
         off = (-self.buf.data_ptr()) % 256
         return self.buf[off:off + nbytes]
 
@@ -403,7 +415,7 @@ def scan_topk(planes: torch.Tensor, qmin: torch.Tensor, qscale: torch.Tensor, q:
     if need == 0:
         _check(L.fathom_scan_topk(ctypes.byref(args), None, 0, _stream(stream)))
     ws = _workspace(workspace, dev)
-    buf = ws.get(need)
+    buf = ws.get(need, stream)
     _check(L.fathom_scan_topk(ctypes.byref(args), _ptr(buf), need, _stream(stream)))
     if debug_scores:
         return out[0], out[1], dbg
@@ -451,7 +463,7 @@ class BatchedScan:
 
     def __call__(self, workspace: Optional[Workspace] = None, stream=None):
         ws = _workspace(workspace, self.device)
-        buf = ws.get(self.need)
+        buf = ws.get(self.need, stream)
         _check(lib().fathom_scan_topk_batched(ctypes.byref(self.args), _ptr(buf), self.need,
                                               _stream(stream)))
         # The descriptor tensor lives as long as this object; the workspace
@@ -691,11 +703,14 @@ def _on(device: torch.device, *tensors: Optional[torch.Tensor]):
 
 
 class _Launch:
-    """The current device and stream of a call on a cache's device.  `new` allocates as
-    torch does, for its current stream; where the call goes to another stream, the
-    allocator is told not to hand the memory out again before that stream has passed."""
+    """The current device and stream of a call on a cache's device.
 
-    __slots__ = ("guard", "stream", "raw")
+    Where the call goes to another stream than torch's current one, its memory comes from
+    that stream's (what the allocator has for the current stream may still be in use by work
+    that is queued there), and the allocator learns that the current stream will use the
+    results (`new`) and the call's stream the arguments (`reads`)."""
+
+    __slots__ = ("guard", "stream", "raw", "home")
 
     def __init__(self, device: torch.device, stream):
         if device.type != "cuda":
@@ -708,16 +723,31 @@ class _Launch:
         self.raw = torch._C._cuda_getCurrentRawStream(device.index)
         self.stream = None
         if stream is not None and stream.cuda_stream != self.raw:
+            self.home = torch.cuda.current_stream(device)
             self.stream, self.raw = stream, stream.cuda_stream
 
     def new(self, like: torch.Tensor, shape=None, dtype=None) -> torch.Tensor:
-        if shape is None and like.is_contiguous():
-            x = torch.empty_like(like)
-        else:
-            x = like.new_empty(like.shape if shape is None else shape, dtype=dtype)
         if self.stream is not None:
-            x.record_stream(self.stream)
-        return x
+            with torch.cuda.stream(self.stream):
+                x = like.new_empty(like.shape if shape is None else shape, dtype=dtype)
+            x.record_stream(self.home)
+            return x
+        if shape is None and like.is_contiguous():
+            return torch.empty_like(like)
+        return like.new_empty(like.shape if shape is None else shape, dtype=dtype)
+
+    def scratch(self, like: torch.Tensor, nbytes: int) -> torch.Tensor:
+        if self.stream is None:
+            return like.new_empty((nbytes,), dtype=torch.uint8)
+        with torch.cuda.stream(self.stream):
+            return like.new_empty((nbytes,), dtype=torch.uint8)
+
+    def reads(self, cache, batch, *tensors: Optional[torch.Tensor]):
+        if self.stream is not None:
+            for x in (cache.k, cache.v, cache.k_scale, cache.v_scale, batch.page_table, batch.seq_len,
+                      batch.q_start) + tensors:
+                if x is not None:
+                    x.record_stream(self.stream)
 
     def __enter__(self):
         return self
@@ -736,7 +766,10 @@ def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, 
     inv_freq float32 [pairs]: pair r of a row at position p turns by p * inv_freq[r]
     (None: no rotation); pair r is dimensions r and r + pairs, or 2r and 2r + 1 with
     interleaved.  Rows may be strided (parts of a fused projection).  Returns the
-    rotated q [num_rows, h_q, d] (None without q); q_out=q rotates in place."""
+    rotated q [num_rows, h_q, d] (None without q); q_out=q rotates in place.
+
+    stream (default: torch's current one) is where the call runs: what it reads must be
+    ready there, and who uses its results elsewhere waits for it."""
     device, rows, d = cache.device, batch.num_rows, cache.d
     _on(device, batch.page_table, k, v, q, inv_freq, q_out)
     ks, vs = _rows_of(k, "k", rows, d), _rows_of(v, "v", rows, d)
@@ -752,6 +785,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, 
     if pairs:
         a.inv_freq, a.rotary_pairs, a.interleaved = inv_freq.data_ptr(), pairs, int(interleaved)
     with _Launch(device, stream) as at:
+        at.reads(cache, batch, k, v, q, inv_freq, q_out)
         if q is not None:
             if q_out is None:
                 q_out = at.new(q)
@@ -773,7 +807,8 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
 
     Returns (out [num_rows, h_q, d] of q's dtype, lse f32 [num_rows, h_q]), neither of
     which may overlap q; rows that no sequence has are left as they were.  Without a workspace the call takes
-    one from torch's allocator, so that two captured graphs never share one."""
+    one from torch's allocator, so that two captured graphs never share one.  stream as
+    for kv_append."""
     device, rows, d = cache.device, batch.num_rows, cache.d
     _on(device, batch.page_table, q, out, lse)
     qs = _rows_of(q, "q", rows, d)
@@ -782,6 +817,7 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
     h_q = q.shape[1]
     L = lib()
     with _Launch(device, stream) as at:
+        at.reads(cache, batch, q, out, lse)
         if out is None:
             out = at.new(q)
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
@@ -795,8 +831,8 @@ def kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor,
         ref = ctypes.byref(a)
         need = L.fathom_kv_attention_workspace_size(ref)
         if workspace is None:
-            ws = at.new(q, (max(need, 1),), torch.uint8)
+            ws = at.scratch(q, max(need, 1))
         else:
-            ws = workspace.get(need)
+            ws = workspace.get(need, at.stream)
         _check(L.fathom_kv_attention(ref, ws.data_ptr(), need, at.raw))
     return out, lse
