@@ -572,7 +572,17 @@ def check_device_status(workspace: Optional[Workspace] = None, device=None, stre
                                             _stream(stream)))
 
 
-class KVCache:
+class _Fixed:
+    """Attributes are set once: the library's arguments are made from them."""
+
+    def __setattr__(self, name, value):
+        if self.__dict__.get(name, value) is not value:  # (x.seq_len += 1 assigns the same tensor)
+            raise AttributeError("%s.%s is fixed: rewrite the tensor in place, or make a new %s"
+                                 % (type(self).__name__, name, type(self).__name__))
+        self.__dict__[name] = value
+
+
+class KVCache(_Fixed):
     """A layer's paged cache of keys and values.
 
     k, v [num_pages, h_kv, page_tokens, d], bfloat16 or float8_e4m3fn, contiguous;
@@ -623,7 +633,7 @@ class KVCache:
                                       dtype=torch.uint8, device=device) for _ in range(2)))
 
 
-class KVBatch:
+class KVBatch(_Fixed):
     """The sequences of one step and their new tokens (rows).
 
     page_table int32 [num_seqs, width]; seq_len int32 [num_seqs], the tokens of
@@ -631,7 +641,7 @@ class KVBatch:
     sequence s has rows q_start[s] .. q_start[s + 1] - 1 (None: one row each).
     All on the GPU, read there only; num_rows, max_rows and max_len are the host's
     bounds on them (defaults: one row each; the tokens that the table can hold).
-    The tensors may be rewritten in place between calls and graph replays."""
+    The tensors may be rewritten in place between calls and graph replays, not replaced."""
 
     def __init__(self, page_table: torch.Tensor, seq_len: torch.Tensor,
                  q_start: Optional[torch.Tensor] = None, *, num_rows: Optional[int] = None,

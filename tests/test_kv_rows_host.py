@@ -1,4 +1,5 @@
-"""Rows that the paged cache's calls refuse before the library sees them (no GPU)."""
+"""Rows that the paged cache's calls refuse before the library sees them, and handles whose
+fields stay (no GPU)."""
 
 import pytest
 import torch
@@ -45,3 +46,18 @@ def test_row_strides():
     assert F._rows_of(torch.zeros((5, 8, 64)), "q", 5, 64) == 512
     assert F._rows_of(torch.zeros((5, 16, 64))[:, 3:11], "q", 5, 64) == 1024
     assert F._rows_of(torch.zeros((0, 8, 64)), "q", 0, 64) == 0
+
+
+def test_handles_keep_what_they_were_made_from():
+    """The library's arguments are made once: a field that is replaced would not be seen."""
+    cache, batch = _setup(5)
+    before = batch.args_for(cache)
+    for name, value in (("seq_len", torch.ones(5, dtype=torch.int32)), ("page_table", batch.page_table.clone()),
+                        ("q_start", torch.arange(6, dtype=torch.int32)), ("num_rows", 4), ("max_rows", 2), ("max_len", 7)):
+        with pytest.raises(AttributeError, match="KVBatch.%s is fixed" % name):
+            setattr(batch, name, value)
+    with pytest.raises(AttributeError, match="KVCache.k is fixed"):
+        cache.k = cache.k.clone()
+    batch.q_start = None    # what it is
+    batch.seq_len += 3      # in place: the same tensor
+    assert batch.args_for(cache) is before and before.seq_len == batch.seq_len.data_ptr()
