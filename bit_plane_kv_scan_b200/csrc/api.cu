@@ -735,7 +735,24 @@ fathom_status fathom_kv_attention(const fathom_kv_attention_args *a, void *ws, s
   int plans;
   fathom_status st = check_kv_attention(a, plan, plans);
   if (st != FATHOM_OK) return st;
-  if (plans == 0) return ok();  // no sequences or no rows
+  if (plans == 0) {  // no sequences or no rows: the status alone, where there is a workspace
+    if (ws == nullptr) return ok();
+    const int dev = current_device();
+    REQUIRE_ON_DEVICE(ws, "workspace", 256);
+    if (ws_bytes < sizeof(WsStatus))
+      return fail(FATHOM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes,
+                  sizeof(WsStatus));
+    if (a->batch.num_seqs > 0) REQUIRE_ON_DEVICE(a->batch.seq_len, "batch.seq_len", 4);
+    if (a->batch.num_seqs > 0 && a->batch.q_start)
+      REQUIRE_ON_DEVICE(a->batch.q_start, "batch.q_start", 4);
+    KvAttnParams p;
+    memset(&p, 0, sizeof(p));
+    p.b = kv_batch_of(a->cache, a->batch);
+    p.status = static_cast<WsStatus *>(ws);
+    const cudaError_t e = launch_kv_status(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
+    return ok();
+  }
   const size_t el = elt_size(a->q_dtype);
   // a unit that is done again reads q after the first time has written out and lse
   const uint64_t rows = a->batch.num_rows, row = (uint64_t)a->h_q * a->cache.d;

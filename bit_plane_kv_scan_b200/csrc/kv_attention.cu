@@ -701,6 +701,13 @@ __global__ void __launch_bounds__(kThreads) kv_join_units_kernel(KvAttnParams a)
   if (lane == 0 && a.lse) a.lse[rh] = lse_of(m, l, 0.0f);
 }
 
+// A call without rows: its status.
+__global__ void __launch_bounds__(kThreads) kv_status_kernel(KvAttnParams a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  write_status(a);
+}
+
 template <int D, bool F8, typename Kernel>
 cudaError_t launch_ring(Kernel kernel, int64_t blocks, const KvAttnParams &a, cudaStream_t s) {
   constexpr int smem = Shape<D, F8>::kSmem;
@@ -888,6 +895,10 @@ int plan_kv_attention(const KvAttnParams &a, bool f8, KvAttnParams (&plan)[2]) {
   }
   plan_one(plan[0], f8);
   return both ? 2 : 1;
+}
+
+cudaError_t launch_kv_status(const KvAttnParams &a, cudaStream_t s) {
+  return launch_dependent(kv_status_kernel, dim3(1), dim3(kThreads), 0, s, a);
 }
 
 cudaError_t launch_kv_attention(const KvAttnParams &a, bool f8, cudaStream_t s) {

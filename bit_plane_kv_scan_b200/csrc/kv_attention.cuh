@@ -150,6 +150,7 @@ __device__ __forceinline__ void write_status(const KvAttnParams &a) {
 }
 
 // kv_attention.cu
+cudaError_t launch_kv_status(const KvAttnParams &a, cudaStream_t s);  // a call without rows
 cudaError_t launch_kv_attention(const KvAttnParams &a, bool f8, cudaStream_t s);
 // The launches of one call, one or two (long and short sequences apart), into plan.
 int plan_kv_attention(const KvAttnParams &a, bool f8, KvAttnParams (&plan)[2]);

@@ -552,7 +552,9 @@ FATHOM_API fathom_status fathom_kv_append(const fathom_kv_append_args *args, voi
  * FATHOM_E4M3 cache need up to 4 GiB of it, for the keys and values that a sequence's
  * rows may see widened to bf16, or one KV head of one sequence where that is more.)  It starts with the status
  * that fathom_check_device_status reads: a sequence that the batch's bounds
- * reject is a device fault, and so is a wait inside a kernel that ran out.
+ * reject is a device fault, and so is a wait inside a kernel that ran out.  (A call
+ * without sequences or rows needs no workspace, and writes the status of one that it
+ * is given.)
  */
 typedef struct fathom_kv_attention_args {
   fathom_kv_cache cache;

@@ -116,3 +116,32 @@ def test_attention_serves_the_sequences_that_keep_their_bounds(name, G, dtype):
     else:
         T.F.check_device_status(ws)
     assert math.isfinite(float(out.float().abs().max()))
+
+
+def test_status_of_a_call_without_rows():
+    """The status is the last call's, also where that had nothing to do."""
+    rng = np.random.default_rng(41)
+    cache = make_cache(rng, 4, 16, 1, 64, BF16)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    ws = T.F.Workspace()
+
+    def call(lens, start, rows):
+        batch = T.F.KVBatch(table, i32(*lens), i32(*start), num_rows=rows, max_rows=min(rows, 1))
+        out, lse = T.F.kv_attention(cache, batch, randn(rng, rows, 2, 64), workspace=ws)
+        assert out.shape == (rows, 2, 64) and lse.shape == (rows, 2)
+
+    ws.buf = torch.full((4096,), 77, dtype=torch.uint8, device="cuda")
+    call((3, 4), (0, 0, 0), 0)
+    T.F.check_device_status(ws)
+    call((3, 99), (0, 1, 2), 2)
+    with pytest.raises(T.F.FathomError, match="1 faults"):
+        T.F.check_device_status(ws)
+    call((3, 4), (0, 0, 0), 0)
+    T.F.check_device_status(ws)
+    call((-3, 400), (0, 0, 0), 0)
+    with pytest.raises(T.F.FathomError, match="2 faults"):
+        T.F.check_device_status(ws)
+    table = table[:0].contiguous()
+    T.F.kv_attention(cache, T.F.KVBatch(table, i32()), randn(rng, 0, 2, 64), workspace=ws)
+    T.F.check_device_status(ws)
