@@ -75,7 +75,9 @@ struct alignas(N == 8 ? 16 : sizeof(T)) Vec {
 __device__ __forceinline__ float2 cos_sin(int p, float f) {
   constexpr double kInvPi = 0.31830988618379067;       // 1 / pi
   constexpr double kInvPiLow = -1.9678676675182486e-17;  // 1 / pi less that
-  const double a = (double)p * (double)f;  // exact: 31 and 24 bits
+  // exact below 2^29; from there on 30 and 24 bits may need one more than fp64 has, and
+  // the product is off by 2^-24 at most where f is at most 1
+  const double a = (double)p * (double)f;
   const double h = a * kInvPi;
   const double low = fma(a, kInvPi, -h) + a * kInvPiLow;
   const double r = (h - 2.0 * rint(0.5 * h)) + low;
@@ -487,6 +489,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendParams 
       } else {
         for_tasks<W, TKV>(lane, 32, m, 1, per, load, store, nothing);
       }
+      __syncwarp();  // every lane has read the older scale
       if (lane == 0) *scale = (uint8_t)x;
     }
   }
