@@ -545,6 +545,8 @@ FATHOM_API fathom_status fathom_kv_append(const fathom_kv_append_args *args, voi
  * fp32.  FATHOM_BF16 queries: softmax weights are rounded to 16 bits before they
  * meet V (bf16; fp16 where few rows read an FATHOM_E4M3 cache).  FATHOM_F32
  * queries and their weights are split into 16-bit terms that keep 22 bits or more.
+ * Weights of up to 2^15 times values are added up before they are divided by the
+ * weights' sum: values of 2^80 and more in magnitude may overflow.
  * Requires h_q a multiple of h_kv, a finite softmax_scale, window >= 0 and
  * sinks >= 0.  The workspace (fathom_kv_attention_workspace_size bytes, 0 on
  * bad arguments) is 256-byte aligned device memory, which the call need not

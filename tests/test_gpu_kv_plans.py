@@ -174,3 +174,71 @@ def test_bounds_far_above_the_lengths(d, h_kv, G, page, lens, rows, window, sink
     exact = T.F.KVBatch(batch.page_table, batch.seq_len, batch.q_start, num_rows=batch.num_rows,
                         max_rows=batch.max_rows, max_len=max(lens))
     check(T.F.kv_attention(cache, exact, q, window=window, sinks=sinks), want)
+
+
+# -------------------------------------------------------- weights and scales --
+
+FEW = [
+    # d, h_kv, G, lens, rows, window, sinks: fewer than 64 columns each
+    (128, 2, 4, [700, 1, 33, 2000], None, 0, 0),
+    (128, 1, 4, [9000], [15], 0, 0),
+    (64, 2, 7, [1500, 400], [9, 3], 200, 5),
+    (96, 1, 1, [300, 90], [63, 20], 0, 0),
+    (160, 1, 8, [500], [5], 0, 0),
+    (256, 1, 2, [800, 60], [31, 2], 100, 3),
+    (128, 2, 4, [900, 500, 100], [15, 2, 1], 2, 0),
+    (64, 2, 8, [900, 500, 100], [7, 2, 1], 3, 2),
+    (128, 8, 1, [700] * 8, None, 33, 0),
+]
+
+
+@pytest.mark.parametrize("d,h_kv,G,lens,rows,window,sinks", FEW)
+def test_few_rows_over_e4m3_have_weights_of_11_bits(d, h_kv, G, lens, rows, window, sinks):
+    """bf16 queries.  Values of either sign, of which a few keys' nearly cancel: there the output's
+    own rounding to bf16 is small, and weights of 8 bits are off by 3 tolerances (windows of 2 to
+    33 keys)."""
+    rng = np.random.default_rng(53)
+    pages = sum(-(-n // 64) for n in lens)
+    cache = make_cache(rng, pages, 64, h_kv, d, F8)
+    batch, table, seqs = make_batch(rng, pages, 64, lens, rows)
+    q = randn(rng, batch.num_rows, h_kv * G, d, scale=1.5)
+    got = T.F.kv_attention(cache, batch, q, window=window, sinks=sinks)
+    want = attention64(cache, table, seqs, q, 1 / math.sqrt(d), window, sinks, 2.0 ** -11)
+    check(got, want)
+    # the weights alone: an fp32 row's output is not rounded, and its weights have 21 bits
+    got = T.F.kv_attention(cache, batch, q.float(), window=window, sinks=sinks)
+    check(got, attention64(cache, table, seqs, q.float(), 1 / math.sqrt(d), window, sinks, 2.0 ** -21, 2.0 ** -24))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, -0.01, 2.0, 1e-30])
+@pytest.mark.parametrize("d,G,rows", [(64, 4, 150), (96, 2, 100), (128, 8, 40), (256, 4, 90)])
+def test_many_rows_with_any_scale(d, G, rows, scale, dtype):
+    rng = np.random.default_rng(54)
+    ct = BF16 if dtype == "bf16" else F8
+    cache = make_cache(rng, 8, 64, 1, d, ct)
+    batch, table, seqs = make_batch(rng, 8, 64, [400], [rows])
+    q = randn(rng, rows, G, d)
+    got = T.F.kv_attention(cache, batch, q, scale, window=150, sinks=4)
+    check(got, attention64(cache, table, seqs, q, scale, 150, 4, WEIGHT[ct, BF16]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 5, 200])
+@pytest.mark.parametrize("power", [79, -80])
+def test_values_far_from_one(power, rows, qt, dtype):
+    """Values just below 2^80, where sums of weights times values may first overflow, and small
+    ones: the result scales with them."""
+    rng = np.random.default_rng(55)
+    ct, qt = BF16 if dtype == "bf16" else F8, BF16 if qt == "bf16" else F32
+    cache = make_cache(rng, 80, 64, 1, 64, ct)
+    if ct == BF16:
+        cache.v.copy_((cache.v.float() / cache.v.float().abs().max() * 2.0 ** power).to(BF16))
+    else:  # |code| < 2^9
+        cache.v_scale.fill_(127 + power - 9)
+    batch, table, seqs = make_batch(rng, 80, 64, [5000], [rows])
+    q = randn(rng, rows, 4, 64, dtype=qt)
+    got = T.F.kv_attention(cache, batch, q)
+    want = attention64(cache, table, seqs, q, 1 / 8, 0, 0, WEIGHT[ct, qt], 2.0 ** -8 if qt == BF16 else 2.0 ** -24)
+    check(got, want)
