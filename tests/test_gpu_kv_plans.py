@@ -29,9 +29,14 @@ def attention64(cache, table, seqs, q, scale, window=0, sinks=0, weight_step=2.0
         if m == 0:
             continue
         held[row0:row0 + m] = True
+        if n == 0:
+            lse[row0:row0 + m] = -math.inf
+            continue
         j = torch.arange(n, device=dev)
         pg = torch.as_tensor(np.asarray(table[s]), device=dev).long()[j // page]
         sl = j % page
+        ok = (pg >= 0) & (pg < cache.k.shape[0])  # tokens whose page exists
+        pg = torch.where(ok, pg, 0)
         for g in range(h_kv):
             kv = []
             for name in ("k", "v"):
@@ -43,20 +48,21 @@ def attention64(cache, table, seqs, q, scale, window=0, sinks=0, weight_step=2.0
                 else:
                     x = x[pg, g, sl].double()
                 kv.append(x)
-            k, v = kv
+            k, v = (torch.where(ok[:, None], x, 0.0) for x in kv)
             heads = slice(g * G, (g + 1) * G)
             for r in range(0, m, 256):
                 e = min(m, r + 256)
                 at = slice(row0 + r, row0 + e)
                 p = torch.arange(n - m + r, n - m + e, device=dev)[:, None]
-                see = j <= p
+                see = (j <= p) & ok
                 if window:
                     see &= (j > p - window) | (j < sinks)
                 see = see[:, None, :]
+                some = see.any(-1)
                 qq = q[at, heads]
                 sc = (qq @ k.T * scale).masked_fill(~see, -math.inf)
                 lse[at, heads] = torch.logsumexp(sc, -1)
-                w = torch.softmax(sc, -1)
+                w = torch.where(some[..., None], torch.softmax(sc, -1), 0.0)
                 out[at, heads] = w @ v
                 a = w @ v.abs()
                 b = (abs(scale) * (qq.abs() @ k.abs().T)).masked_fill(~see, 0.0).amax(-1)
@@ -67,7 +73,7 @@ def attention64(cache, table, seqs, q, scale, window=0, sinks=0, weight_step=2.0
                     + out_step * out[at, heads].abs() + 1e-30
                 if weight_step == 2.0 ** -11:
                     tol[at, heads] += 2.0 ** -40 * (see.double() @ v.abs())
-                ltol[at, heads] = delta + 2.0 ** -20 + adds * 2.0 ** -23 + 2.0 ** -22 * lse[at, heads].abs().clamp(min=1)
+                ltol[at, heads] = delta + 2.0 ** -20 + adds * 2.0 ** -23 + 2.0 ** -22 * torch.where(some, lse[at, heads], 0.0).abs().clamp(min=1)
     return out, lse, tol, ltol, held
 
 
@@ -75,7 +81,10 @@ def check(got, want, what=""):
     out, lse, tol, ltol, held = want
     e = ((got[0].double() - out).abs() / tol.clamp(min=1e-30))[held].max().item()
     assert e <= 1, "%s: out off by %g tolerances" % (what, e)
-    e = ((got[1].double() - lse).abs() / ltol.clamp(min=1e-30))[held].max().item()
+    nothing = torch.isneginf(lse)
+    assert (got[0][nothing & held[:, None]] == 0).all() and torch.isneginf(got[1][nothing & held[:, None]]).all(), what
+    lse, mine = torch.where(nothing, 0.0, lse), torch.where(nothing, 0.0, got[1].double())
+    e = ((mine - lse).abs() / ltol.clamp(min=1e-30))[held].max().item()
     assert e <= 1, "%s: lse off by %g tolerances" % (what, e)
 
 
@@ -242,3 +251,63 @@ def test_values_far_from_one(power, rows, qt, dtype):
     got = T.F.kv_attention(cache, batch, q)
     want = attention64(cache, table, seqs, q, 1 / 8, 0, 0, WEIGHT[ct, qt], 2.0 ** -8 if qt == BF16 else 2.0 ** -24)
     check(got, want)
+
+
+# ------------------------------------------------------------- what is missing --
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,G,page", [(128, 4, 64), (64, 8, 16), (256, 4, 128), (96, 4, 48)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 20)])
+def test_many_rows_with_pages_and_tokens_missing(d, G, page, window, sinks, dtype):
+    """Pages outside the pool in the middle and at the end, more rows than tokens, an empty
+    sequence with rows; the workspace and the pages that nobody has are full of NaNs."""
+    rng = np.random.default_rng(56)
+    ct = BF16 if dtype == "bf16" else F8
+    lens, rows = [700, 150, 0, 384], [300, 200, 70, 384]
+    pages = sum(-(-n // page) for n in lens) + 3
+    cache = make_cache(rng, pages, page, 1, d, ct)
+    batch, _, _ = make_batch(rng, pages, page, lens, rows)
+    table = batch.page_table.cpu().numpy()
+    width = table.shape[1]
+    free = sorted(set(range(pages)) - set(table[table >= 0].tolist()))
+    for at, bad in ((250 // page, -1), (460 // page, pages), (690 // page, 1 << 30)):
+        free.append(int(table[0, at]))
+        table[0, at] = bad
+    free.append(int(table[3, 0]))
+    table[3, 0] = -(1 << 31)
+    for x in (cache.k, cache.v):
+        if ct == BF16:
+            x[free] = math.nan
+        else:
+            x.view(torch.uint8)[free] = 0x7f
+    batch.page_table.copy_(torch.from_numpy(table))
+    seqs = [(sum(rows[:i]), rows[i], lens[i]) for i in range(4)]
+    q = randn(rng, sum(rows), G, d)
+    ws = T.F.Workspace()
+    ws.get(64 << 20).fill_(255)
+    got = T.F.kv_attention(cache, batch, q, window=window, sinks=sinks, workspace=ws)
+    assert width == table.shape[1] and ws.buf.numel() == (64 << 20) + 256
+    check(got, attention64(cache, table, seqs, q, 1 / math.sqrt(d), window, sinks, WEIGHT[ct, BF16]))
+    T.F.check_device_status(ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("m,bad,window,sinks", [(6, 196, 0, 0), (200, 120, 0, 0), (150, 60, 50, 3), (150, 2, 50, 3)])
+def test_a_key_that_is_not_finite_spoils_the_rows_that_see_it(m, bad, window, sinks, dtype):
+    rng = np.random.default_rng(57)
+    n, page = 200, 64
+    cache = make_cache(rng, 5, page, 2, 128, BF16 if dtype == "bf16" else F8)
+    batch, table, _ = make_batch(rng, 5, page, [n], [m])
+    q = randn(rng, m, 8, 128)
+    want = T.F.kv_attention(cache, batch, q, window=window, sinks=sinks)
+    at = (table[0][bad // page], 1, bad % page)  # of KV head 1
+    if dtype == "bf16":
+        cache.k[at] = math.nan
+    else:
+        cache.k.view(torch.uint8)[at] = 0x7f
+    got = T.F.kv_attention(cache, batch, q, window=window, sinks=sinks)
+    p = torch.arange(n - m, n, device="cuda")
+    sees = (bad <= p) & ((p - bad < window) | (bad < sinks) if window else torch.ones_like(p, dtype=torch.bool))
+    assert sees.any() and torch.isnan(got[0][sees, 4:]).all()
+    for g, w in zip(got, want):
+        assert torch.equal(g[:, :4], w[:, :4]) and torch.equal(g[~sees], w[~sees])
