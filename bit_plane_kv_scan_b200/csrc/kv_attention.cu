@@ -30,7 +30,10 @@
 // fp16 by a power of two per row and head; a 16-key tile is one scale block, so
 // K's scale multiplies S and V's multiplies that tile's product in fp32.
 // Softmax weights are rounded to fp16 after a factor 2^15, which keeps weights
-// down to 2^-29 of the largest to 11 bits.  bf16: weights are rounded to bf16.
+// down to 2^-29 of the largest to 11 bits (smaller ones are off by 2^-40 of it).
+// bf16: weights are rounded to bf16, since a product's operands have one type and V
+// does not fit in fp16's range; out is off by 0.0017 of its size with its own rounding
+// to bf16, which alone makes it 0.0017 too.  Their sum is of the weights before that.
 // fp32 queries: q and the weights are split into 2 (fp16) or 3 (bf16) terms and
 // the products run once for each.
 //
@@ -774,7 +777,10 @@ cudaError_t launch_d(const KvAttnParams &a, bool f8, cudaStream_t s) {
 }  // namespace
 
 // Blocks of the few-rows kernel that the device holds at once, by shared memory
-// (228 KB an SM, 1 KB of it for each block).
+// (228 KB an SM, 1 KB of it for each block).  bf16 queries up to 128 dimensions have
+// no more registers than that allows; fp32 queries and more dimensions have up to 255
+// a thread, which is two or three blocks an SM where this says three or four, and their
+// grids are up to two waves.
 static int kv_resident_blocks(int d, bool f8) {
   const int row = f8 ? d : 2 * d;
   const int smem = kWarps * ring_depth(row) * 2 * kKvBlock * (row + 16) + 1280;
@@ -842,9 +848,10 @@ static void plan_one(KvAttnParams &a, bool f8) {
     }
     if (splits > most / 8) splits = most / 8;
   } else {
-    // Runs of at least 4 tiles a warp.  Where every sequence goes through about the
-    // same number of tiles (a window), as many blocks as the SMs hold at once; where
-    // lengths differ from the bound and from each other, smaller runs, so that the
+    // Runs of at least 4 tiles a warp, sized by max_len.  Where every sequence goes
+    // through about the same number of tiles (a window), as many blocks as the SMs hold
+    // at once, rounded up to whole units (64 windowed sessions: 512 on 444 places);
+    // where lengths differ from the bound and from each other, smaller runs, so that the
     // SMs end together (24 sessions of 4096 to 65536 tokens: 501 us with one block
     // a place, 357 with 2, 309 with 4, 292 with 8; one session, 64 windowed ones: 1
     // to 4 are within 1%, 8 costs 2 and 6%).

@@ -495,7 +495,7 @@ typedef struct fathom_kv_batch {
  *   q        optional [num_rows][h_q][d] of q_dtype (FATHOM_BF16 or
  *            FATHOM_F32), rows q_stride elements apart (0: h_q * d); rotated
  *            into q_out [num_rows][h_q][d], which may be q itself where
- *            q_stride is h_q * d, and otherwise must not overlap it.
+ *            q_stride is h_q * d, and otherwise must not overlap it; nor k or v.
  * FATHOM_BF16 cache: each element rounded once.  FATHOM_E4M3 cache: a block's
  * scale is the smallest power of two with max |x| <= 256 * scale over the
  * block's new finite elements as they came (turning a pair grows an element by
@@ -545,18 +545,19 @@ FATHOM_API fathom_status fathom_kv_append(const fathom_kv_append_args *args, voi
  * fp32.  FATHOM_BF16 queries: softmax weights are rounded to 16 bits before they
  * meet V (bf16; fp16 where few rows read an FATHOM_E4M3 cache).  FATHOM_F32
  * queries and their weights are split into 16-bit terms that keep 22 bits or more.
+ * (fp16 weights and terms hold no less than 2^-40 of the row's largest weight.)
  * Weights of up to 2^15 times values are added up before they are divided by the
  * weights' sum: values of 2^80 and more in magnitude may overflow.
  * Requires h_q a multiple of h_kv, a finite softmax_scale, window >= 0 and
  * sinks >= 0.  The workspace (fathom_kv_attention_workspace_size bytes, 0 on
  * bad arguments) is 256-byte aligned device memory, which the call need not
  * find cleared; calls sharing one must not overlap.  (Many rows over an
- * FATHOM_E4M3 cache need up to 4 GiB of it, for the keys and values that a sequence's
- * rows may see widened to bf16, or one KV head of one sequence where that is more.)  It starts with the status
- * that fathom_check_device_status reads: a sequence that the batch's bounds
- * reject is a device fault, and so is a wait inside a kernel that ran out.  (A call
- * without sequences or rows needs no workspace, and writes the status of one that it
- * is given.)
+ * FATHOM_E4M3 cache need up to 4 GiB of it, or one KV head of one sequence where that
+ * is more, for the keys and values that rows may see, widened to bf16; else it is some
+ * tens of MB at most.)  It starts with the status that fathom_check_device_status
+ * reads: a sequence that the batch's bounds reject is a device fault, and so is a wait
+ * inside a kernel that ran out.  (A call without sequences or rows needs no workspace,
+ * and writes the status of one that it is given.)
  */
 typedef struct fathom_kv_attention_args {
   fathom_kv_cache cache;
