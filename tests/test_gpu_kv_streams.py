@@ -1,6 +1,8 @@
 """The paged cache's calls on another stream than torch's current one, while work is queued on
 that one: neither may use memory that the other still uses."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -113,3 +115,71 @@ def test_a_workspace_knows_the_streams_it_was_used_on():
     assert ws._home == side.cuda_stream
     ws.get(9000)
     assert ws._home == torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_a_forked_stream_inside_a_capture(dtype):
+    """Append on the captured stream, two attentions side by side on it and on a stream that
+    forks from it; replays after other work has used the memory in between."""
+    cache, batch, q = _setup(dtype, [9000, 1500, 300], [1, 200, 2])
+    rng = np.random.default_rng(62)
+    k, v = (randn(rng, batch.num_rows, 2, 128) for _ in range(2))
+    f = torch.full((64,), 0.01, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        qr = T.F.kv_append(cache, batch, k, v, q=q, inv_freq=f)
+        side.wait_stream(here)
+        full = T.F.kv_attention(cache, batch, qr, stream=side)
+        win = T.F.kv_attention(cache, batch, qr, window=200, sinks=4)
+        here.wait_stream(side)
+        return (qr, *full, *win)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        for x in (k, v, q):
+            x.copy_(randn(rng, *x.shape))
+        _dirt(q.numel() * 2, 1 << 20)
+        g.replay()
+        torch.cuda.synchronize()
+        held = [x.clone() for x in got]
+        want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(held, want):
+            assert torch.equal(a, b)
+
+
+def test_calls_from_several_threads():
+    """Each thread with a stream of its own, calls of every kind at once."""
+    jobs = [_setup(d, lens, rows) for d, lens, rows in (
+        ("bf16", [9000, 300], None), ("e4m3", [9000, 300], None), ("bf16", [1500, 40], [600, 1]),
+        ("e4m3", [1500, 40], [600, 1]))]
+    want = [T.F.kv_attention(*j) for j in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for n in range(20):
+                    j = (i + n) % len(jobs)
+                    with pytest.raises(T.F.FathomError, match="negative"):
+                        T.F.kv_attention(*jobs[j], window=-1 - i)
+                    got = T.F.kv_attention(*jobs[j])
+                    torch.cuda.current_stream().synchronize()
+                    if not (torch.equal(got[0], want[j][0]) and torch.equal(got[1], want[j][1])):
+                        wrong.append((i, n))
+        except BaseException as e:  # noqa: B902
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
