@@ -725,6 +725,8 @@ class _Launch:
     def __init__(self, device: torch.device, stream):
         if device.type != "cuda":
             raise ValueError("the cache is on %s, not on a CUDA device" % device)
+        if stream is not None and stream.device != device:  # (default streams' handles are alike)
+            raise ValueError("the cache is on %s, the stream on %s" % (device, stream.device))
         self.guard = None
         if torch._C._cuda_getDevice() != device.index:
             self.guard = torch.cuda.device(device)

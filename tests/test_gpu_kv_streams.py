@@ -2,6 +2,7 @@
 that one: neither may use memory that the other still uses."""
 
 import threading
+import types
 
 import numpy as np
 import pytest
@@ -183,3 +184,14 @@ def test_calls_from_several_threads():
     for t in threads:
         t.join()
     assert not wrong, wrong[:3]
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The default streams of two devices have one handle: the device decides."""
+    cache, batch, q = _setup("bf16", [300], None)
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="the stream on cuda:1"):
+        T.F.kv_attention(cache, batch, q, stream=other)
+    with pytest.raises(ValueError, match="the stream on cuda:1"):
+        T.F.kv_append(cache, batch, q[:, :2], q[:, :2], stream=other)
+    T.F.kv_attention(cache, batch, q, stream=torch.cuda.default_stream())
